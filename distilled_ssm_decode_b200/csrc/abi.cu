@@ -257,9 +257,11 @@ int hyena_debug_bounds_check(long long *record) {
     int (*const readers[])(long long *) = {bounds_read_decode, bounds_read_filter, bounds_read_fir,
                                            bounds_read_prefill_chunked, bounds_read_prefill_fft,
                                            bounds_read_state, bounds_read_truncate,
-                                           bounds_read_prefill_monarch};
+                                           bounds_read_prefill_monarch, bounds_read_linattn,
+                                           bounds_read_linattn_decode,
+                                           bounds_read_qk_norm};
     int found = 0;
-    for (int f = 0; f < 8; ++f) {
+    for (int f = 0; f < (int)(sizeof(readers) / sizeof(readers[0])); ++f) {
         long long rec[4];
         const int r = readers[f](rec);      // every record is read (and cleared), the first one kept
         if (r < 0) return HYENA_ERR_CUDA;
@@ -453,6 +455,103 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
                                              reinterpret_cast<float2 *>(lambda_out),
                                              reinterpret_cast<float2 *>(R_out), bound, err_l2,
                                              (cudaStream_t)stream));
+}
+
+static int check_linattn(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
+    if (dtype != HYENA_F32 && dtype != HYENA_BF16) return HYENA_ERR_ARG;
+    if (B < 0 || L < 0 || H < 1 || Hk < 1 || H % Hk != 0 || dk < 1 || dv < 1) return HYENA_ERR_SHAPE;
+    if (dk > HYENA_MAX_HEAD_DIM || B > 65535) return HYENA_ERR_UNSUPPORTED;
+    if ((long long)H * dv > 0x7fffffffll || (long long)H * dk > 0x7fffffffll) return HYENA_ERR_UNSUPPORTED;
+    return HYENA_OK;
+}
+
+static int check_strides(int H, int Hk, int dk, int dv, long long ldq, long long ldk, long long ldv) {
+    return ldq < (long long)H * dk || ldk < (long long)Hk * dk || ldv < (long long)Hk * dv ? HYENA_ERR_SHAPE : HYENA_OK;
+}
+
+static int check_prep(const hyena_qk_prep *p, int hd) {
+    if (p->rot_dim < 0 || p->rot_dim > hd || p->rot_dim % 2 || hd % 2) return HYENA_ERR_SHAPE;
+    if ((p->norm != 0 && p->norm != 1) || (p->interleaved != 0 && p->interleaved != 1)) return HYENA_ERR_ARG;
+    if (!(p->eps >= 0.f) || (p->rot_dim > 0 && !p->inv_freq)) return HYENA_ERR_ARG;
+    if (!aligned(p->q_weight, 4) || !aligned(p->k_weight, 4) || !aligned(p->inv_freq, 4)) return HYENA_ERR_ALIGN;
+    return HYENA_OK;
+}
+
+size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
+    if (check_linattn(dtype, B, L, H, Hk, dk, dv) != HYENA_OK) return 0;
+    return linattn_ws_bytes(dtype, B, L, H, Hk, dk, dv);
+}
+
+int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk, int dk,
+                          int dv, long long ldq, long long ldk, long long ldv, const float *decay, float scale,
+                          const int *lens, const float *state_in, void *o, float *state_out, void *workspace,
+                          size_t ws_bytes, hyena_stream_t stream) {
+    int st = check_linattn(dtype, B, L, H, Hk, dk, dv);
+    if (st == HYENA_OK) st = check_strides(H, Hk, dk, dv, ldq, ldk, ldv);
+    if (st != HYENA_OK) return st;
+    if (B == 0) return HYENA_OK;
+    if (!state_out || !decay) return HYENA_ERR_ARG;
+    const size_t sa = dv % 4 == 0 ? 16 : 4;
+    if (!aligned(state_out, sa) || !aligned(state_in, sa) || !aligned(decay, 4) || !aligned(lens, 4)) return HYENA_ERR_ALIGN;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (L == 0) {
+        const size_t n = (size_t)B * Hk * dk * dv * sizeof(float);
+        if (state_in == state_out) return HYENA_OK;
+        HYENA_LAUNCH_GUARD();
+        return cuda_status(state_in ? cudaMemcpyAsync(state_out, state_in, n, cudaMemcpyDeviceToDevice, s)
+                                    : cudaMemsetAsync(state_out, 0, n, s));
+    }
+    if (!q || !k || !v || !o || !workspace) return HYENA_ERR_ARG;
+    const size_t ab = (dtype == HYENA_BF16) ? 2 : 4;
+    if (!aligned(q, ab) || !aligned(k, ab) || !aligned(v, ab) || !aligned(o, ab) || !aligned(workspace, kAlign))
+        return HYENA_ERR_ALIGN;
+    if (ws_bytes < linattn_ws_bytes(dtype, B, L, H, Hk, dk, dv)) return HYENA_ERR_WORKSPACE;
+    HYENA_LAUNCH_GUARD();
+    return cuda_status(launch_linattn_prefill(q, k, v, dtype, B, L, H, Hk, dk, dv, ldq, ldk, ldv, decay, scale, lens,
+                                              state_in, o, state_out, workspace, s));
+}
+
+int hyena_linattn_decode_step(const void *q, const void *k, const void *v, int dtype, int B, int H, int Hk, int dk,
+                              int dv, long long ldq, long long ldk, long long ldv, const float *decay, float scale,
+                              const hyena_qk_prep *prep, const int *positions, int pos0, float *state, void *o,
+                              hyena_stream_t stream) {
+    int st = check_linattn(dtype, B, 1, H, Hk, dk, dv);
+    if (st == HYENA_OK) st = check_strides(H, Hk, dk, dv, ldq, ldk, ldv);
+    if (st == HYENA_OK && prep) st = check_prep(prep, dk);
+    if (st != HYENA_OK) return st;
+    if (B == 0) return HYENA_OK;
+    if (!q || !k || !v || !o || !state || !decay) return HYENA_ERR_ARG;
+    const size_t ab = (dtype == HYENA_BF16) ? 2 : 4;
+    if (!aligned(q, ab) || !aligned(k, ab) || !aligned(v, ab) || !aligned(o, ab) ||
+        !aligned(state, dv % 4 == 0 ? 16 : 4) || !aligned(decay, 4) || !aligned(positions, 4))
+        return HYENA_ERR_ALIGN;
+    HYENA_LAUNCH_GUARD();
+    return cuda_status(launch_linattn_decode(q, k, v, dtype, B, H, Hk, dk, dv, ldq, ldk, ldv, decay, scale, prep,
+                                             positions, pos0, state, o, (cudaStream_t)stream));
+}
+
+int hyena_qk_norm_rotate(const void *q, const void *k, int dtype, int B, int L, int H, int Hk, int hd, long long ldq,
+                         long long ldk, const hyena_qk_prep *prep, const int *positions, int pos0, void *q_out,
+                         void *k_out, long long ldqo, long long ldko, hyena_stream_t stream) {
+    if (dtype != HYENA_F32 && dtype != HYENA_BF16) return HYENA_ERR_ARG;
+    if (!prep) return HYENA_ERR_ARG;
+    if (B < 0 || L < 0 || H < 0 || Hk < 0 || hd < 1) return HYENA_ERR_SHAPE;
+    if (hd > HYENA_MAX_HEAD_DIM) return HYENA_ERR_UNSUPPORTED;
+    if (((long long)H + Hk) * hd > 0x7fffffffll) return HYENA_ERR_UNSUPPORTED;
+    const int st = check_prep(prep, hd);
+    if (st != HYENA_OK) return st;
+    if (ldq < (long long)H * hd || ldqo < (long long)H * hd || ldk < (long long)Hk * hd || ldko < (long long)Hk * hd)
+        return HYENA_ERR_SHAPE;
+    if (B == 0 || L == 0 || H + Hk == 0) return HYENA_OK;
+    if ((H > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out))) return HYENA_ERR_ARG;
+    // in place needs the same rows: another stride would read what an earlier row has written
+    if ((H > 0 && q == q_out && ldq != ldqo) || (Hk > 0 && k == k_out && ldk != ldko)) return HYENA_ERR_ARG;
+    const size_t ab = (dtype == HYENA_BF16) ? 2 : 4;
+    if (!aligned(q, ab) || !aligned(k, ab) || !aligned(q_out, ab) || !aligned(k_out, ab) || !aligned(positions, 4))
+        return HYENA_ERR_ALIGN;
+    HYENA_LAUNCH_GUARD();
+    return cuda_status(launch_qk_norm(q, k, dtype, B, L, H, Hk, hd, ldq, ldk, *prep, positions, pos0, q_out, k_out, ldqo,
+                                      ldko, (cudaStream_t)stream));
 }
 
 }  // extern "C"

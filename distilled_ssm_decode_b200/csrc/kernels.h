@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include "hyena.h"
+
 namespace hyena {
 
 // Largest FFT handled by one CTA in shared memory; longer transforms take the
@@ -100,14 +102,35 @@ cudaError_t launch_fir_step(const void *q, const void *k, const void *v, int dty
 cudaError_t launch_modal_truncate(const float2 *lam, const float2 *R, int H, int d, int k, int *kept,
                                   float2 *lam_out, float2 *R_out, double *bound, double *err_l2, cudaStream_t s);
 
+// linattn.cu (linear attention with a decay for each head, over a prompt)
+size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
+cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk,
+                                   int dk, int dv, long long ldq, long long ldk, long long ldv, const float *decay,
+                                   float scale, const int *lens, const float *state_in, void *o, float *state_out,
+                                   void *ws, cudaStream_t s);
+
+// linattn_decode.cu
+cudaError_t launch_linattn_decode(const void *q, const void *k, const void *v, int dtype, int B, int H, int Hk, int dk,
+                                  int dv, long long ldq, long long ldk, long long ldv, const float *decay, float scale,
+                                  const hyena_qk_prep *p, const int *pos, int pos0, float *state, void *o,
+                                  cudaStream_t s);
+
+// qk_norm.cu
+cudaError_t launch_qk_norm(const void *q, const void *k, int dtype, int B, int L, int H, int Hk, int hd, long long ldq,
+                           long long ldk, const hyena_qk_prep &p, const int *pos, int pos0, void *qo, void *ko,
+                           long long ldqo, long long ldko, cudaStream_t s);
+
 // bounds-checked build: per source file, read and clear the record of the first global access
 // out of range (see common.cuh); in the release build they report nothing
 int bounds_read_decode(long long *rec);
 int bounds_read_filter(long long *rec);
 int bounds_read_fir(long long *rec);
+int bounds_read_linattn(long long *rec);
+int bounds_read_linattn_decode(long long *rec);
 int bounds_read_prefill_chunked(long long *rec);
 int bounds_read_prefill_fft(long long *rec);
 int bounds_read_prefill_monarch(long long *rec);
+int bounds_read_qk_norm(long long *rec);
 int bounds_read_state(long long *rec);
 int bounds_read_truncate(long long *rec);
 

@@ -24,6 +24,7 @@ _lock = threading.Lock()
 _lib = None
 
 _vp, _fp, _i, _sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_ll, _f = ctypes.c_longlong, ctypes.c_float
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -59,6 +60,12 @@ SIGNATURES = {
                                       _vp]),
     "hyena_fir_cache_prompt": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _fp, _vp]),
     "hyena_fir_decode_step": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _fp, _fp, _vp, _vp]),
+    "hyena_linattn_prefill_workspace_bytes": (_sz, [_i] * 7),
+    "hyena_linattn_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _fp, _vp, _fp,
+                                   _vp, _sz, _vp]),
+    "hyena_linattn_decode_step": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _vp, _i, _fp,
+                                       _vp, _vp]),
+    "hyena_qk_norm_rotate": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _ll, _ll, _vp, _vp, _i, _vp, _vp, _ll, _ll, _vp]),
     "hyena_modal_truncate": (_i, [_fp, _fp, _i, _i, _i, _vp, _fp, _fp, _vp, _vp, _vp]),
 }
 
@@ -462,3 +469,178 @@ def modal_truncate(lam, R, k: int):
                                       _ptr(err), _stream(dev)))
     return kept, lo, ro, bound, err
 
+
+
+# ------------------------------------------------------------------ linear attention
+def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
+    """Row stride (elements between consecutive tokens) of q, k or v [B][L][heads][width] (dim 4) or
+    [B][heads][width] (dim 3): heads and width contiguous, rows evenly spaced, as a slice of one
+    projection's output has them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    sh, st = t.shape, t.stride()
+    width, n = sh[-1], sh[-2] * sh[-1]
+    if t.numel() == 0:
+        return n
+    if (width > 1 and st[-1] != 1) or (sh[-2] > 1 and st[-2] != width):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if dim == 3:
+        ld = st[0] if sh[0] > 1 else n
+    elif sh[1] > 1:
+        ld = st[1]
+        if sh[0] > 1 and st[0] != sh[1] * ld:
+            raise ValueError(f"{name}: batch rows must follow each other at the token stride")
+    else:
+        ld = st[0] if sh[0] > 1 else n
+    if ld < n:
+        raise ValueError(f"{name}: tokens overlap")
+    return ld
+
+
+def _plain(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this dtype, shape and device (None passes)."""
+    if t is None:
+        return None
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _on(device):
+    """The library works on the current device: make it the tensors' one for a call."""
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+
+
+class _CQKPrep(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("interleaved", ctypes.c_int)]
+
+
+class QKPrep:
+    """What qk_norm_rotate does to each head of the queries and keys (keep one beside the weights).
+
+    wq, wk: float32 [hd] norm weights (None: ones); eps inside the square root; norm=False leaves
+    the norm out.  inv_freq: float32 [rot_dim / 2], the angle per position of each pair (None: no
+    rotation); interleaved pairs are (2i, 2i+1), else (i, i + rot_dim / 2)."""
+
+    def __init__(self, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False, norm: bool = True):
+        for name, t in (("wq", wq), ("wk", wk), ("inv_freq", inv_freq)):
+            if t is not None and _cuda(t, name, torch.float32).dim() != 1:
+                raise ValueError(f"{name} must have one dimension")
+        self.wq, self.wk, self.inv_freq = wq, wk, inv_freq
+        self.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+        at = lambda t: t.data_ptr() if t is not None and t.numel() else None
+        self._c = _CQKPrep(int(norm), eps, at(wq), at(wk), self.rot_dim, at(inv_freq), int(interleaved))
+        self._ref = ctypes.c_void_p(ctypes.addressof(self._c))
+
+    def _check(self, hd: int, device):
+        for name, t in (("wq", self.wq), ("wk", self.wk)):
+            if t is not None and (t.numel() != hd or t.device != device):
+                raise ValueError(f"{name} must be [{hd}] on {device}")
+        if self.inv_freq is not None and self.inv_freq.device != device:
+            raise ValueError(f"inv_freq must be on {device}")
+        return self._ref
+
+
+def qk_norm_rotate(q, k, prep: QKPrep, positions=None, pos0: int = 0, q_out=None, k_out=None):
+    """Norm of each head of q [B][L][H][hd] and k [B][L][Hk][hd], and the position rotation, in one
+    pass.  positions int32 [B][L], or None: token t stands at pos0 + t.  q_out=q, k_out=k work in
+    place.  Returns (q_out, k_out)."""
+    dt, dev = _act_dtype(q), q.device
+    ldq, ldk = _rows(q, "q", 4, q.dtype, dev), _rows(k, "k", 4, q.dtype, dev)
+    B, L, H, hd = q.shape
+    Hk = k.shape[2]
+    if k.shape[:2] != q.shape[:2] or k.shape[3] != hd:
+        raise ValueError("q and k must be [B][L][heads][hd] with the same B, L and hd")
+    _plain(positions, "positions", torch.int32, (B, L), dev)
+    if q_out is None:
+        q_out = torch.empty((B, L, H, hd), dtype=q.dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty((B, L, Hk, hd), dtype=q.dtype, device=dev)
+    ldqo, ldko = _rows(q_out, "q_out", 4, q.dtype, dev), _rows(k_out, "k_out", 4, q.dtype, dev)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    with _on(dev):
+        _check("hyena_qk_norm_rotate",
+               lib().hyena_qk_norm_rotate(_ptr(q), _ptr(k), dt, B, L, H, Hk, hd, ldq, ldk, prep._check(hd, dev),
+                                          _ptr(positions), pos0, _ptr(q_out), _ptr(k_out), ldqo, ldko, _stream(dev)))
+    return q_out, k_out
+
+
+def linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv) -> int:
+    return int(lib().hyena_linattn_prefill_workspace_bytes(_DT[dtype], B, L, H, Hk, dk, dv))
+
+
+def linattn_prefill(q, k, v, decay, scale: float = 1.0, lens=None, state_in=None, o=None, state=None, workspace=None):
+    """Linear attention with a decay for each head over a prompt: S_t = g S_{t-1} + k_t v_t^T,
+    o_t = scale S_t^T q_t.
+
+    q [B][L][H][dk], k [B][L][Hk][dk], v [B][L][Hk][dv] (slices of one projection work), decay float32
+    [Hk], lens int32 [B] (tokens of each row; the rows of o behind them are left as they were, zero
+    if o is made here), state_in float32 [B][Hk][dk][dv].  Returns (o [B][L][H][dv], state)."""
+    dt, dev = _act_dtype(q), q.device
+    ldq, ldk, ldv = _rows(q, "q", 4, q.dtype, dev), _rows(k, "k", 4, q.dtype, dev), _rows(v, "v", 4, q.dtype, dev)
+    B, L, H, dk = q.shape
+    Hk, dv = v.shape[2:]
+    if k.shape != (B, L, Hk, dk) or v.shape[:2] != (B, L):
+        raise ValueError("q [B][L][H][dk], k [B][L][Hk][dk], v [B][L][Hk][dv] expected")
+    _plain(decay, "decay", torch.float32, (Hk,), dev)
+    _plain(lens, "lens", torch.int32, (B,), dev)
+    _plain(state_in, "state_in", torch.float32, (B, Hk, dk, dv), dev)
+    if o is None:
+        o = (torch.empty if lens is None else torch.zeros)((B, L, H, dv), dtype=q.dtype, device=dev)
+    if state is None:
+        state = torch.empty((B, Hk, dk, dv), dtype=torch.float32, device=dev)
+    _plain(o, "o", q.dtype, (B, L, H, dv), dev)
+    _plain(state, "state", torch.float32, (B, Hk, dk, dv), dev)
+    with _on(dev):
+        if workspace is None:
+            nbytes = linattn_prefill_workspace_bytes(q.dtype, B, L, H, Hk, dk, dv)
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        _cuda(workspace, "workspace", torch.uint8)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+        _check("hyena_linattn_prefill",
+               lib().hyena_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), dt, B, L, H, Hk, dk, dv, ldq, ldk, ldv, _ptr(decay),
+                                           scale, _ptr(lens), _ptr(state_in), _ptr(o), _ptr(state), _ptr(workspace),
+                                           workspace.numel(), _stream(dev)))
+    return o, state
+
+
+def linattn_decode_step(q, k, v, decay, state, scale: float = 1.0, prep: QKPrep = None, positions=None, pos0: int = 0,
+                        o=None):
+    """One token: S <- g S + k v^T (state [B][Hk][dk][dv] in place), o = scale S^T q.
+
+    q [B][H][dk], k [B][Hk][dk], v [B][Hk][dv] (slices of one projection work).  With prep, q and k pass
+    through qk_norm_rotate's formulas in the same launch, at positions int32 [B] (None: pos0).
+    Returns o [B][H][dv]."""
+    dt, dev = _act_dtype(q), q.device
+    ldq, ldk, ldv = _rows(q, "q", 3, q.dtype, dev), _rows(k, "k", 3, q.dtype, dev), _rows(v, "v", 3, q.dtype, dev)
+    B, H, dk = q.shape
+    Hk, dv = v.shape[1:]
+    if k.shape != (B, Hk, dk) or v.shape[0] != B:
+        raise ValueError("q [B][H][dk], k [B][Hk][dk], v [B][Hk][dv] expected")
+    if state is None:
+        raise TypeError("state must be a CUDA tensor")
+    _plain(decay, "decay", torch.float32, (Hk,), dev)
+    _plain(state, "state", torch.float32, (B, Hk, dk, dv), dev)
+    _plain(positions, "positions", torch.int32, (B,), dev)
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+    _plain(o, "o", q.dtype, (B, H, dv), dev)
+    with _on(dev):
+        _check("hyena_linattn_decode_step",
+               lib().hyena_linattn_decode_step(_ptr(q), _ptr(k), _ptr(v), dt, B, H, Hk, dk, dv, ldq, ldk, ldv, _ptr(decay),
+                                               scale, None if prep is None else prep._check(dk, dev), _ptr(positions),
+                                               pos0, _ptr(state), _ptr(o), _stream(dev)))
+    return o

@@ -271,7 +271,8 @@ int hyena_prefill_chunked_layers(int layers, const void *const *q, const void *c
  * and clears the records.  Returns 0 when no access was out of range, 1 when
  * one was, with record = {file, source line, index, extent} (file: 1 decode.cu,
  * 2 filter.cu, 3 fir.cu, 4 prefill_chunked.cu, 5 prefill_fft.cu, 6 state.cu,
- * 7 truncate.cu, 8 prefill_monarch.cu); HYENA_ERR_UNSUPPORTED from the release build, which has no
+ * 7 truncate.cu, 8 prefill_monarch.cu, 9 linattn.cu, 10 linattn_decode.cu,
+ * 11 qk_norm.cu); HYENA_ERR_UNSUPPORTED from the release build, which has no
  * checks; HYENA_ERR_ARG for a NULL record.
  */
 int hyena_debug_bounds_check(long long *record);
@@ -420,6 +421,96 @@ int hyena_fir_decode_step(const void *q, const void *k, const void *v, int dtype
 int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int k, int *kept,
                          float *lambda_out, float *R_out, double *bound, double *err_l2,
                          hyena_stream_t stream);
+
+/*
+ * Linear attention with a decay for each head: the outer-product form of the
+ * recurrence above.  Every key/value head keeps a matrix state S [dk][dv] with
+ * one real decay g = decay[head], 0 <= g <= 1:
+ *     S_t = g S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t
+ * H query heads share Hk key/value heads (H a multiple of Hk): query head h
+ * reads the state of head h / (H / Hk).  decay is [Hk].
+ *
+ * hyena_linattn_prefill takes a prompt and hands its state to generation:
+ *   q         : [B][L][H][dk],  k : [B][L][Hk][dk],  v : [B][L][Hk][dv] (dtype).
+ *               A token's heads are contiguous; consecutive tokens are ldq, ldk,
+ *               ldv elements apart (>= H dk, Hk dk, Hk dv; batch rows L tokens
+ *               apart), so the three may be slices of one projection.
+ *   decay     : [Hk] fp32 device
+ *   lens      : [B] int32 device, or NULL: only the first lens[b] tokens of row b
+ *               (clamped to 0..L) belong to the sequence.  What q, k, v hold
+ *               behind them is never used; the rows of o behind them are left as
+ *               they were.  NULL: all L tokens.
+ *   state_in  : [B][Hk][dk][dv] fp32, or NULL for a zero state.  May be state_out.
+ *   o         : [B][L][H][dv] (dtype), contiguous
+ *   state_out : [B][Hk][dk][dv] fp32, overwritten with the state after the last
+ *               token (state_in, or zero, for an empty sequence)
+ *   workspace : device scratch, >= hyena_linattn_prefill_workspace_bytes() bytes,
+ *               256-byte aligned; contents on entry are ignored.  Calls that may
+ *               overlap need one each.
+ * 1 <= dk <= HYENA_MAX_HEAD_DIM, 1 <= dv, H dv and Hk dv < 2^31; B <= 65535.
+ * Alignment: q, k, v, o to their element size, states 16 bytes (4 when dv is
+ * not a multiple of 4), decay and lens 4.
+ * Runs in fp32 on the CUDA cores.
+ * Empty problems (B == 0, or L == 0) are valid; L == 0 writes state_out.
+ */
+#define HYENA_MAX_HEAD_DIM 256
+
+size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
+int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype,
+                          int B, int L, int H, int Hk, int dk, int dv,
+                          long long ldq, long long ldk, long long ldv,
+                          const float *decay, float scale, const int *lens, const float *state_in,
+                          void *o, float *state_out,
+                          void *workspace, size_t ws_bytes, hyena_stream_t stream);
+
+/*
+ * Norm of queries and keys for each head, and the position rotation, in one pass:
+ *     x <- x * rsqrt(mean(x^2) + eps) * weight        (over one head's hd entries)
+ *     (a, b) <- (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
+ * for the rot_dim / 2 pairs of the first rot_dim entries: (x_i, x_{i + rot_dim/2}),
+ * or (x_2i, x_{2i+1}) if interleaved.  Angles are formed and reduced in fp64, so far
+ * positions keep their accuracy; the rest is fp32, rounded once on store.
+ */
+typedef struct {
+    int norm;                 /* 1: norm, 0: x as it is */
+    float eps;                /* >= 0 */
+    const float *q_weight;    /* [hd] fp32 device, or NULL (ones) */
+    const float *k_weight;
+    int rot_dim;              /* even, 0 (no rotation) .. hd */
+    const float *inv_freq;    /* [rot_dim / 2] fp32 device */
+    int interleaved;
+} hyena_qk_prep;
+
+/*
+ *   q : [B][L][H][hd],  k : [B][L][Hk][hd] (dtype), rows ldq, ldk elements apart as
+ *       for hyena_linattn_prefill; q_out, k_out the same shapes with rows ldqo,
+ *       ldko apart.  q_out == q with ldqo == ldq (and the same for k) works in place.
+ *       H == 0 or Hk == 0: only the other one (its pointers may be NULL).
+ *   positions : [B][L] int32 device, or NULL: token t stands at pos0 + t.
+ *   prep is a HOST struct, read during the call.  hd even, <= HYENA_MAX_HEAD_DIM.
+ */
+int hyena_qk_norm_rotate(const void *q, const void *k, int dtype, int B, int L, int H, int Hk, int hd,
+                         long long ldq, long long ldk, const hyena_qk_prep *prep,
+                         const int *positions, int pos0, void *q_out, void *k_out,
+                         long long ldqo, long long ldko, hyena_stream_t stream);
+
+/*
+ * One token of the recurrence for a batch of sequences:
+ *     S <- g S + k v^T,    o = scale * S^T q
+ *   q : [B][H][dk], k : [B][Hk][dk], v : [B][Hk][dv] (dtype), batch rows ldq, ldk, ldv
+ *   elements apart; o : [B][H][dv] (dtype), contiguous; state : [B][Hk][dk][dv] fp32,
+ *   updated in place.
+ *   prep : NULL, or q and k pass through hyena_qk_norm_rotate's formulas on the way
+ *   (kept in fp32, in the same launch); positions : [B] int32 device, or NULL: every
+ *   row stands at pos0.  With prep, dk must be even.
+ * Sizes and alignment as for hyena_linattn_prefill.
+ */
+int hyena_linattn_decode_step(const void *q, const void *k, const void *v, int dtype,
+                              int B, int H, int Hk, int dk, int dv,
+                              long long ldq, long long ldk, long long ldv,
+                              const float *decay, float scale,
+                              const hyena_qk_prep *prep, const int *positions, int pos0,
+                              float *state, void *o, hyena_stream_t stream);
 
 #ifdef __cplusplus
 }
