@@ -102,8 +102,11 @@ cudaError_t launch_fir_step(const void *q, const void *k, const void *v, int dty
 cudaError_t launch_modal_truncate(const float2 *lam, const float2 *R, int H, int d, int k, int *kept,
                                   float2 *lam_out, float2 *R_out, double *bound, double *err_l2, cudaStream_t s);
 
-// linattn.cu (linear attention with a decay for each head, over a prompt)
-size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
+// linattn.cu, linattn_tc.cu (linear attention with a decay for each head, over a prompt)
+size_t linattn_ws_bytes(int dtype, int B, int L, int Hk, int dk, int dv);
+size_t linattn_err_offset(int dtype, int B, int L, int Hk, int dk, int dv);
+bool linattn_uses_tc(int dtype, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
+                     const void *k, const void *v, const void *o);
 cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk,
                                    int dk, int dv, long long ldq, long long ldk, long long ldv, const float *decay,
                                    float scale, const int *lens, const float *state_in, void *o, float *state_out,
@@ -127,6 +130,7 @@ int bounds_read_filter(long long *rec);
 int bounds_read_fir(long long *rec);
 int bounds_read_linattn(long long *rec);
 int bounds_read_linattn_decode(long long *rec);
+int bounds_read_linattn_tc(long long *rec);
 int bounds_read_prefill_chunked(long long *rec);
 int bounds_read_prefill_fft(long long *rec);
 int bounds_read_prefill_monarch(long long *rec);

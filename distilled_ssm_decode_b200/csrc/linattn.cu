@@ -1,4 +1,5 @@
-// linattn.cu -- linear attention with a decay for each head over a prompt.
+// linattn.cu -- linear attention with a decay for each head over a prompt: the CUDA-core route, the
+// split of long prompts into segments (both routes), and the launcher.
 //
 // Mathematics, for a block of T tokens with entering state S (g the head's decay):
 //   o_t = scale (g^(t+1) S^T q_t + sum_{j<=t} g^(t-j) (q_t . k_j) v_j),   t = 0..T-1
@@ -255,17 +256,30 @@ cudaError_t launch_simt(const LinArgs &a, bool states_only, cudaStream_t s) {
 
 HYENA_BOUNDS_READER(linattn)
 
-size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
-    (void)dtype; (void)H;
-    const LinPlan p = simt_plan(B, L, Hk, dv);
-    return al256(p.nseg > 1 ? (size_t)p.nseg * B * Hk * dk * dv * sizeof(float) : 0) + 256;
+bool linattn_uses_tc(int dtype, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
+                     const void *k, const void *v, const void *o) {
+    auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    return linattn_tc_dims(dtype, dk, dv) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0 && ok(q) && ok(k) && ok(v) && ok(o);
+}
+
+// Workspace: [segment states][error words of the state pass][error words of the main pass].  The queries know
+// neither strides nor pointers, so there is room for whichever route is taken.
+size_t linattn_err_offset(int dtype, int B, int L, int Hk, int dk, int dv) {
+    int nseg = simt_plan(B, L, Hk, dv).nseg;
+    if (linattn_tc_dims(dtype, dk, dv)) nseg = max(nseg, linattn_tc_plan(B, L, Hk, dv).nseg);
+    return al256(nseg > 1 ? (size_t)nseg * B * Hk * dk * dv * sizeof(float) : 0);
+}
+
+size_t linattn_ws_bytes(int dtype, int B, int L, int Hk, int dk, int dv) {
+    return linattn_err_offset(dtype, B, L, Hk, dk, dv) + 2 * kLinMaxBlocks * sizeof(int);
 }
 
 cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk,
                                    int dk, int dv, long long ldq, long long ldk, long long ldv, const float *decay,
                                    float scale, const int *lens, const float *state_in, void *o, float *state_out,
                                    void *ws, cudaStream_t s) {
-    LinPlan p = simt_plan(B, L, Hk, dv);
+    const bool tc = linattn_uses_tc(dtype, dk, dv, ldq, ldk, ldv, q, k, v, o);
+    const LinPlan p = tc ? linattn_tc_plan(B, L, Hk, dv) : simt_plan(B, L, Hk, dv);
     LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.o = o;
     a.B = B; a.L = L; a.H = H; a.Hk = Hk; a.dk = dk; a.dv = dv;
@@ -275,8 +289,13 @@ cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, 
     a.seg_tokens = p.seg_tokens; a.nseg = p.nseg; a.vtiles = p.vtiles;
     a.init_stride = (long long)B * Hk * dk * dv;
     a.states = static_cast<float *>(ws);
+    int *err = reinterpret_cast<int *>(static_cast<char *>(ws) + linattn_err_offset(dtype, B, L, Hk, dk, dv));
     auto run = [&](bool states_only) {
-        return dtype == HYENA_BF16 ? launch_simt<ActBF16>(a, states_only, s) : launch_simt<ActF32>(a, states_only, s);
+        // both sets of words are written when there is no state pass
+        a.err = states_only || p.nseg == 1 ? err : err + kLinMaxBlocks;
+        a.nerr = p.nseg == 1 ? 2 * kLinMaxBlocks : kLinMaxBlocks;
+        return tc ? launch_linattn_tc(a, states_only, s)
+                  : dtype == HYENA_BF16 ? launch_simt<ActBF16>(a, states_only, s) : launch_simt<ActF32>(a, states_only, s);
     };
     if (p.nseg > 1) {
         cudaError_t e = run(true);

@@ -1,4 +1,4 @@
-// linattn.cuh -- arguments and plan of the linear-attention prefill.
+// linattn.cuh -- arguments and plan shared by the two routes of the linear-attention prefill.
 #pragma once
 
 #include "common.cuh"
@@ -31,6 +31,8 @@ struct LinArgs {
     float *state_out;        // else: the state after the last segment
     int seg_tokens, nseg;    // segments of this launch (states_only leaves out the last one)
     int vtiles;              // column tiles of a state
+    int *err;                // tensor-core route: an error word for each block
+    int nerr;
 };
 
 // tokens of row b
@@ -45,5 +47,11 @@ __device__ __forceinline__ int row_tokens(const LinArgs &a, int b) {
 struct LinPlan {
     int vtiles, nseg, seg_tokens;
 };
+
+// linattn_tc.cu
+constexpr int kLinMaxBlocks = 148;       // one block per SM
+bool linattn_tc_dims(int dtype, int dk, int dv);
+LinPlan linattn_tc_plan(int B, int L, int Hk, int dv);
+cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s);
 
 }  // namespace hyena

@@ -1,0 +1,618 @@
+// linattn_tc.cu -- linear attention with a decay for each head over a prompt, on the tensor cores.
+//
+// Per chunk of n <= C = 128 tokens with entering state S [dk][dv] (g the head's decay, i, j in the chunk):
+//   A_ij = q_i . k_j                                           (scores)
+//   P_ij = scale g^(i-j) A_ij for j <= i, else 0
+//   O    = diag(scale g^(i+1)) (Q S) + P V
+//   S    <- g^n S + sum_j (g^(n-1-j) k_j) v_j^T
+// an exact regrouping of S <- g S + k v^T, o = scale S^T q.  All weights are powers of g in [0, 1].
+//
+// Four products per chunk, accumulated in fp32 in tensor memory:
+//   scores  128 x 128 x dk   Q (shared) x K (shared)            -> columns kColP
+//   Q S     128 x dv x dk    Q (shared) x S as bf16 (shared)    -> columns kColO, then scaled in place
+//   P V     128 x dv x n     P as bf16 (tensor memory, over the scores) x V (shared), onto kColO
+//   state   dk x dv x n      weighted keys (tensor memory) x V (shared), onto the scaled state in kColS
+// Roundings to bf16: the scores' P and the state's copy that multiplies q (operands only; both reach o, itself bf16).
+// The state stays fp32 in tensor memory from chunk to chunk; its weighted keys are the sum of three bf16
+// terms (24 bits), so that it is as exact as an fp32 sum: one term would leave 2^-9, two 2^-17 of each token in a
+// state that every later token reads.
+//
+// Bound: 2 (dk + dv) (1 + 1) bytes per token and head of q, k, v, o against 2 C (dk + dv) + (2 + 6) dk dv operations:
+// memory-bound (at dk = dv = 128 the products need 55% of the time that the bytes need), if the chain
+// scores -> P -> P V -> o of a chunk overlaps the loads of the next and the state's own chain.  Hence one
+// persistent block per SM (a chunk's tiles fill shared memory) with a role for each warp group:
+//   warp 0 loads K, V; warp 1 loads Q; warp 2 issues every product; warp 3 stores O
+//   warps 4-7   P group: a token row per thread: scores -> P, scaling of Q S, then O -> shared memory
+//   warps 8-11  K group: a row of the state (an entry of k) per thread: weighted keys -> tensor memory
+//   warps 12-15 S group: a row of the state per thread: the state's bf16 copy, its decay, its load and store
+// They meet at mbarriers only.  Every wait is bounded; on timeout the block records it in its error word,
+// drains its copies and products, frees tensor memory and returns.
+//
+// Tensor-memory rows: tokens for the first three products, entries of k for the state.  With dk <= 64 the state's
+// rows 64..127 hold what the unused lanes give; nothing reads them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include "linattn.cuh"
+#include "tc.cuh"
+
+namespace hyena {
+
+namespace {
+
+constexpr int kC = 128;                 // tokens of a chunk
+constexpr int kThreads = 512;
+constexpr int kBlk = kC * 128;          // bytes of a [128 tokens][64 entries] bf16 tile, 128-byte swizzled
+constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColW = 384;   // tensor-memory columns
+constexpr uint32_t kTmemCols = 512;
+constexpr int kTerms = 3;               // bf16 terms of a weighted key
+constexpr int kHalf = 64;               // tokens of weighted keys held at a time: kTerms x 32 columns
+
+struct Maps {
+    CUtensorMap q, k, v, o;
+};
+
+template <int NK, int NV>
+struct Geo {
+    static constexpr int kKB = NK / 64, kVB = NV / 64;                 // 64-entry blocks
+    static constexpr int kStage = (kKB + kVB) * kBlk;                  // K, then V
+    static constexpr int kQSlot = (kKB > kVB ? kKB : kVB) * kBlk;      // Q, then O
+    static constexpr int kStages = 2, kQSlots = 2;
+    static constexpr int kSBytes = NK * NV * 2;
+    static constexpr int kSmQ = kStages * kStage;
+    static constexpr int kSmS = kSmQ + kQSlots * kQSlot;
+    static constexpr int kSmPw = kSmS + kSBytes;                       // float pw[kC + 4], rev[32], rw[kC]
+    static constexpr int kSmBar = kSmPw + 4 * (kC + 4 + 32 + kC);
+    enum { KVFull = 0, KVEmpty = KVFull + kStages, QFull = KVEmpty + kStages, QEmpty = QFull + kQSlots,
+           OStaged = QEmpty + kQSlots, T1Done = OStaged + kQSlots, PReady, T2Done, OFree, WReady, WFree, SReady, SFree,
+           T3Done, Drain, kNumBars };
+    static constexpr int kSmMisc = kSmBar + 8 * kNumBars;
+    static constexpr int kSmem = kSmMisc + 16 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kSmBar % 8 == 0 && kSmS % 1024 == 0, "alignment");
+    __host__ __device__ static constexpr int count(int b) {
+        return (b >= OStaged && b < T1Done) || b == PReady || b == OFree || b == WReady || b == SReady ? 128 : 1;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&p);
+}
+__device__ __forceinline__ float lo_of(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+struct Item {
+    int seg, b, hk, c0, t0, ntok, nck;      // first column, first token, tokens, chunks
+};
+
+__device__ __forceinline__ Item item_of(const LinArgs &a, int id, int nv) {
+    Item it;
+    it.c0 = (id % a.vtiles) * nv;
+    id /= a.vtiles;
+    it.hk = id % a.Hk;
+    id /= a.Hk;
+    it.b = id % a.B;
+    it.seg = id / a.B;
+    const int len = row_tokens(a, it.b);
+    it.t0 = (int)min((long long)len, (long long)it.seg * a.seg_tokens);
+    it.ntok = min(len - it.t0, a.seg_tokens);
+    it.nck = (it.ntok + kC - 1) / kC;
+    return it;
+}
+
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads, 1)
+linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int items, const int states_only) {
+    using G = Geo<NK, NV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = tc::smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *pw = reinterpret_cast<float *>(sm + G::kSmPw);            // pw[n] = g^n
+    float *rev = pw + kC + 4;                                        // rev[x] = g^(31 - x)
+    float *rw = rev + 32;                                            // rw[x] = g^(kC - 1 - x) (the K group's)
+    volatile int *misc = reinterpret_cast<volatile int *>(sm + G::kSmMisc);   // abort (= error code), tensor memory, never
+    volatile int *abort = misc, *never = misc + 2;
+    auto bar = [&](int b) { return sbase + G::kSmBar + 8u * b; };
+    const int Gq = a.H / a.Hk;
+
+    if (tid == 0) {
+        misc[0] = 0;
+        misc[2] = 0;
+        for (int i = 0; i < G::kNumBars; ++i) tc::mbar_init(bar(i), G::count(i));
+        tc::fence_mbar_init();
+    } else if (tid == 32) {
+        tc::prefetch_tensormap(&m.q);
+        tc::prefetch_tensormap(&m.k);
+        tc::prefetch_tensormap(&m.v);
+        tc::prefetch_tensormap(&m.o);
+    }
+    if (warp == 2) {
+        tc::tmem_alloc(tc::smem_u32((const void *)(misc + 1)), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = (uint32_t)misc[1];
+    auto uni = [&](bool x) -> bool { return __all_sync(0xffffffffu, x && !*abort); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K, V loads
+        if (lane == 0) {
+            int cc = 0;
+            bool ok = true;
+            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                const Item it = item_of(a, id, NV);
+                for (int c = 0; c < it.nck; ++c, ++cc) {
+                    const int st = cc % G::kStages;
+                    if (!(ok = tc::mbar_wait(bar(G::KVEmpty + st), ((cc / G::kStages) & 1) ^ 1, abort))) break;
+                    const uint32_t dst = sbase + st * G::kStage;
+                    tc::mbar_expect_tx(bar(G::KVFull + st), G::kStage);
+                    for (int x = 0; x < G::kKB; ++x)
+                        tc::tma_load_4d(dst + x * kBlk, &m.k, bar(G::KVFull + st), 64 * x, it.hk, it.t0 + c * kC, it.b);
+                    for (int x = 0; x < G::kVB; ++x)
+                        tc::tma_load_4d(dst + (G::kKB + x) * kBlk, &m.v, bar(G::KVFull + st), it.c0 + 64 * x, it.hk,
+                                        it.t0 + c * kC, it.b);
+                }
+            }
+            if (!ok) {
+                *abort = 1;
+                for (int j = max(0, cc - G::kStages); j < cc; ++j)
+                    tc::mbar_wait(bar(G::KVFull + j % G::kStages), (j / G::kStages) & 1, never);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ Q loads
+        if (lane == 0 && !states_only) {
+            int qc = 0;
+            bool ok = true;
+            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                const Item it = item_of(a, id, NV);
+                for (int c = 0; c < it.nck && ok; ++c)
+                    for (int x = 0; x < Gq; ++x, ++qc) {
+                        const int s = qc % G::kQSlots;
+                        if (!(ok = tc::mbar_wait(bar(G::QEmpty + s), ((qc / G::kQSlots) & 1) ^ 1, abort))) break;
+                        tc::mbar_expect_tx(bar(G::QFull + s), G::kKB * kBlk);
+                        for (int y = 0; y < G::kKB; ++y)
+                            tc::tma_load_4d(sbase + G::kSmQ + s * G::kQSlot + y * kBlk, &m.q, bar(G::QFull + s), 64 * y,
+                                            it.hk * Gq + x, it.t0 + c * kC, it.b);
+                    }
+            }
+            if (!ok) {
+                *abort = 1;
+                for (int j = max(0, qc - G::kQSlots); j < qc; ++j)
+                    tc::mbar_wait(bar(G::QFull + j % G::kQSlots), (j / G::kQSlots) & 1, never);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            int cc = 0, qc = 0, wc = 0;
+            bool ok = true;
+            const uint32_t id_score = tc::idesc_bf16(128, 128, false), id_v = tc::idesc_bf16(128, NV, true);
+            auto wait = [&](int b, int phase) { return ok = ok && tc::mbar_wait(bar(b), phase & 1, abort); };
+            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                const Item it = item_of(a, id, NV);
+                for (int c = 0; c < it.nck && ok; ++c, ++cc) {
+                    const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
+                    const uint32_t k_at = sbase + st * G::kStage, v_at = k_at + G::kKB * kBlk;
+                    const bool has_state = c > 0 || (a.init && !states_only);
+                    if (!wait(G::KVFull + st, cc / G::kStages) || !wait(G::SReady, cc)) break;
+                    // state: the weighted keys of up to 64 tokens at a time
+                    auto state_product = [&]() {
+                        for (int h = 0; h * kHalf < n; ++h, ++wc) {
+                            if (!wait(G::WReady, wc)) return;
+                            tc::tc_fence_after();
+                            const int ks_end = min(kHalf / 16, steps - h * (kHalf / 16));
+                            for (int ks = 0; ks < ks_end; ++ks) {
+                                const uint64_t vd = tc::smem_desc_sw128(v_at + (h * (kHalf / 16) + ks) * 2048, kBlk, 1024);
+#pragma unroll
+                                for (int t = 0; t < kTerms; ++t)
+                                    tc::mma_bf16_ta(tmem + kColS, tmem + kColW + 32 * t + 8 * ks, vd, id_v, 1);
+                            }
+                            tc::mma_commit(bar(G::WFree));
+                        }
+                        tc::mma_commit(bar(G::T3Done));
+                    };
+                    if (states_only) {
+                        state_product();
+                    } else {
+                        for (int x = 0; x < Gq && ok; ++x, ++qc) {
+                            const int s = qc % G::kQSlots;
+                            if (!wait(G::QFull + s, qc / G::kQSlots) || !wait(G::OFree, qc + 1)) break;
+                            tc::tc_fence_after();
+                            const uint32_t q_at = sbase + G::kSmQ + s * G::kQSlot;
+#pragma unroll
+                            for (int ks = 0; ks < NK / 16; ++ks) {
+                                const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
+                                tc::mma_bf16(tmem + kColP, tc::smem_desc_sw128(q_at + off, 16, 1024),
+                                             tc::smem_desc_sw128(k_at + off, 16, 1024), id_score, ks > 0);
+                            }
+                            if (has_state) {
+#pragma unroll
+                                for (int ks = 0; ks < NK / 16; ++ks) {
+                                    const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
+                                    tc::mma_bf16(tmem + kColO, tc::smem_desc_sw128(q_at + off, 16, 1024),
+                                                 tc::smem_desc_sw128(sbase + G::kSmS + ks * 2048, NK * 128, 1024), id_v, ks > 0);
+                                }
+                            }
+                            tc::mma_commit(bar(G::T1Done));
+                            if (x == Gq - 1) tc::mma_commit(bar(G::SFree));
+                            if (x == 0) state_product();
+                            if (!wait(G::PReady, qc)) break;
+                            tc::tc_fence_after();
+                            for (int ks = 0; ks < steps; ++ks)
+                                tc::mma_bf16_ta(tmem + kColO, tmem + kColP + 8 * ks, tc::smem_desc_sw128(v_at + ks * 2048, kBlk, 1024),
+                                                id_v, has_state || ks > 0);
+                            tc::mma_commit(bar(G::T2Done));
+                        }
+                    }
+                    tc::mma_commit(bar(G::KVEmpty + st));
+                }
+            }
+            if (!ok) *abort = 1;
+            tc::mma_commit(bar(G::Drain));
+            tc::mbar_wait(bar(G::Drain), 0, never);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ O stores (whole chunks)
+        if (lane == 0 && !states_only) {
+            int qc = 0, prev = -1;
+            bool ok = true;
+            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                const Item it = item_of(a, id, NV);
+                for (int c = 0; c < it.nck && ok; ++c)
+                    for (int x = 0; x < Gq; ++x, ++qc) {
+                        const int s = qc % G::kQSlots;
+                        if (!(ok = tc::mbar_wait(bar(G::OStaged + s), (qc / G::kQSlots) & 1, abort))) break;
+                        if (it.ntok - c * kC >= kC)
+                            for (int y = 0; y < G::kVB; ++y)
+                                if (it.c0 + 64 * y < a.dv)
+                                    tc::tma_store_4d(&m.o, sbase + G::kSmQ + s * G::kQSlot + y * kBlk, it.c0 + 64 * y,
+                                                     it.hk * Gq + x, it.t0 + c * kC, it.b);
+                        tc::bulk_commit();
+                        tc::bulk_wait_read<0>();
+                        tc::mbar_arrive(bar(G::QEmpty + s));
+                        prev = s;
+                    }
+            }
+            (void)prev;
+            if (!ok) *abort = 1;
+            tc::bulk_wait<0>();
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ P group
+        const int w = warp & 3, row = 32 * w + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+        int qc = 0, hk_cur = -1;
+        bool ok = !states_only;
+        for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+            const Item it = item_of(a, id, NV);
+            // the head's powers (this group writes its own table for itself)
+            if (it.hk != hk_cur && it.nck > 0) {
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
+                pw[row] = (float)decay_pow(g, row);
+                if (row == 0) pw[kC] = (float)decay_pow(g, kC);
+                if (row < 32) rev[row] = (float)decay_pow(g, 31 - row);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                hk_cur = it.hk;
+            }
+            for (int c = 0; c < it.nck && ok; ++c) {
+                const int n = min(kC, it.ntok - c * kC);
+                const bool has_state = c > 0 || a.init;
+                for (int x = 0; x < Gq; ++x, ++qc) {
+                    if (!(ok = uni(tc::mbar_wait(bar(G::T1Done), qc & 1, abort)))) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (32 * p >= n) break;
+                        uint32_t out[16];
+                        if (p > w) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) out[j] = 0;      // later tokens
+                        } else {
+                            float z[32];
+                            tc::tmem_ld32(lane_base + kColP + 32 * p, z);
+                            tc::tmem_wait_ld();
+                            if (p < w) {
+                                const float f = a.scale * pw[row - (32 * p + 31)];
+#pragma unroll
+                                for (int j = 0; j < 32; j += 4) {
+                                    const float4 r4 = *reinterpret_cast<const float4 *>(rev + j);
+                                    out[j / 2] = pack2(z[j] * (f * r4.x), z[j + 1] * (f * r4.y));
+                                    out[j / 2 + 1] = pack2(z[j + 2] * (f * r4.z), z[j + 3] * (f * r4.w));
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    const float y0 = j <= lane ? z[j] * (a.scale * pw[max(lane - j, 0)]) : 0.f;
+                                    const float y1 = j + 1 <= lane ? z[j + 1] * (a.scale * pw[max(lane - j - 1, 0)]) : 0.f;
+                                    out[j / 2] = pack2(y0, y1);
+                                }
+                            }
+                        }
+                        tc::tmem_st16(lane_base + kColP + 16 * p, out);
+                    }
+                    if (has_state) {
+                        const float f = a.scale * pw[row + 1];
+#pragma unroll
+                        for (int p = 0; p < NV / 32; ++p) {
+                            float z[32];
+                            tc::tmem_ld32(lane_base + kColO + 32 * p, z);
+                            tc::tmem_wait_ld();
+                            uint32_t out[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) out[j] = __float_as_uint(f * z[j]);
+                            tc::tmem_st32(lane_base + kColO + 32 * p, out);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bar(G::PReady));
+                    if (!(ok = uni(tc::mbar_wait(bar(G::T2Done), qc & 1, abort)))) break;
+                    tc::tc_fence_after();
+                    const int s = qc % G::kQSlots;
+                    uint8_t *ob = sm + G::kSmQ + s * G::kQSlot + row * 128;
+                    const long long at = (((long long)it.b * a.L + it.t0 + c * kC + row) * a.H + it.hk * Gq + x) * a.dv + it.c0;
+#pragma unroll
+                    for (int p = 0; p < NV / 32; ++p) {
+                        float z[32];
+                        tc::tmem_ld32(lane_base + kColO + 32 * p, z);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint4 v4 = make_uint4(pack2(z[8 * y], z[8 * y + 1]), pack2(z[8 * y + 2], z[8 * y + 3]),
+                                                        pack2(z[8 * y + 4], z[8 * y + 5]), pack2(z[8 * y + 6], z[8 * y + 7]));
+                            const int ch = 4 * p + y;               // 16-byte piece of the row
+                            if (n == kC)
+                                *reinterpret_cast<uint4 *>(ob + (ch / 8) * kBlk + (((ch & 7) ^ (row & 7)) << 4)) = v4;
+                            else if (row < n && it.c0 + 8 * ch < a.dv &&
+                                     HB_OK(at + 8 * ch + 7, (long long)a.B * a.L * a.H * a.dv))
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at + 8 * ch) = v4;
+                        }
+                    }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bar(G::OFree));
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(bar(G::OStaged + s));
+                }
+            }
+        }
+        if (!ok && !states_only) *abort = 1;
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ K group
+        const int w = warp & 3, d = 32 * w + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+        int cc = 0, wc = 0, hk_cur = -1;
+        bool ok = true;
+        for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+            const Item it = item_of(a, id, NV);
+            if (it.hk != hk_cur && it.nck > 0) {
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                rw[d] = (float)decay_pow((double)a.decay[HB_IDX(it.hk, a.Hk)], kC - 1 - d);
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                hk_cur = it.hk;
+            }
+            for (int c = 0; c < it.nck && ok; ++c, ++cc) {
+                const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC);
+                if (!(ok = uni(tc::mbar_wait(bar(G::KVFull + st), (cc / G::kStages) & 1, abort)))) break;
+                uint8_t *kt = sm + st * G::kStage;
+                if (n & 15) {
+                    // rows of V behind the last token, up to the products' step of 16: whatever they hold must not
+                    // reach a sum
+                    uint8_t *vt = kt + G::kKB * kBlk;
+                    const int rows = 16 - (n & 15);
+                    for (int i = tid - 256; i < rows * 8 * G::kVB; i += 128)
+                        *reinterpret_cast<uint4 *>(vt + (i / (rows * 8)) * kBlk + (n + (i / 8) % rows) * 128 + (i & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    tc::fence_proxy_async_smem();
+                }
+                for (int h = 0; h * kHalf < n; ++h, ++wc) {
+                    if (!(ok = uni(tc::mbar_wait(bar(G::WFree), (wc & 1) ^ 1, abort)))) break;
+                    tc::tc_fence_after();
+                    if (32 * w < NK) {
+                        const uint8_t *col = kt + (d / 64) * kBlk + (d & 7) * 2;
+                        const int ch = (d & 63) >> 3;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t t0[16], t1[16], t2[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float r[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int t = h * kHalf + 32 * y + 2 * j + e;
+                                    const uint16_t kb = *reinterpret_cast<const uint16_t *>(col + t * 128 + ((ch ^ (t & 7)) << 4));
+                                    // g^(n-1-t)
+                                    r[e] = t < n ? __uint_as_float((uint32_t)kb << 16) * rw[min(t + kC - n, kC - 1)] : 0.f;
+                                }
+                                t0[j] = pack2(r[0], r[1]);
+                                r[0] -= lo_of(t0[j]);
+                                r[1] -= hi_of(t0[j]);
+                                t1[j] = pack2(r[0], r[1]);
+                                r[0] -= lo_of(t1[j]);
+                                r[1] -= hi_of(t1[j]);
+                                t2[j] = pack2(r[0], r[1]);
+                            }
+                            tc::tmem_st16(lane_base + kColW + 16 * y, t0);
+                            tc::tmem_st16(lane_base + kColW + 32 + 16 * y, t1);
+                            tc::tmem_st16(lane_base + kColW + 64 + 16 * y, t2);
+                        }
+                        tc::tmem_wait_st();
+                    }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bar(G::WReady));
+                }
+            }
+        }
+        if (!ok) *abort = 1;
+    } else {
+        // ------------------------------------------------------------ S group
+        const int w = warp & 3, d = 32 * w + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+        int cc = 0;
+        bool ok = true;
+        const long long ns = (long long)a.B * a.Hk * a.dk * a.dv;
+        (void)ns;
+        for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+            const Item it = item_of(a, id, NV);
+            const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
+            const float g_all = (float)decay_pow(g, kC), g_last = (float)decay_pow(g, it.ntok - (it.nck - 1) * kC);
+            const long long at = (((long long)it.b * a.Hk + it.hk) * a.dk + d) * a.dv + it.c0;
+            const float *init = states_only || !a.init ? nullptr : a.init + (long long)it.seg * a.init_stride;
+            float *dst = states_only ? a.states + (long long)(it.seg + 1) * a.init_stride
+                                     : it.seg == a.nseg - 1 ? a.state_out : nullptr;
+            auto load_init = [&](int p, float *z) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const int col = it.c0 + 32 * p + j;
+                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (init && d < a.dk && col < a.dv) t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + 32 * p + j, ns - 3));
+                    z[j] = t.x; z[j + 1] = t.y; z[j + 2] = t.z; z[j + 3] = t.w;
+                }
+            };
+            for (int c = 0; c <= it.nck && ok; ++c) {
+                // the state entering chunk c (or leaving the last one)
+                if (c > 0) {
+                    if (!(ok = uni(tc::mbar_wait(bar(G::T3Done), (cc - 1) & 1, abort)))) break;
+                    tc::tc_fence_after();
+                }
+                if (c == it.nck) {
+                    if (dst) {
+#pragma unroll
+                        for (int p = 0; p < NV / 32; ++p) {
+                            float z[32];
+                            if (c > 0) {
+                                tc::tmem_ld32(lane_base + kColS + 32 * p, z);
+                                tc::tmem_wait_ld();
+                            } else {
+                                load_init(p, z);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                if (d < a.dk && it.c0 + 32 * p + j < a.dv && HB_OK(at + 32 * p + j + 3, ns))
+                                    *reinterpret_cast<float4 *>(dst + at + 32 * p + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                        }
+                    }
+                    tc::tc_fence_before();
+                    break;
+                }
+                const bool has_state = c > 0 || init;
+                // every product with the last chunk's copy is done
+                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+                const float gn = c == it.nck - 1 ? g_last : g_all;
+                if (32 * w < NK) {
+                    uint8_t *row = sm + G::kSmS + d * 128;
+#pragma unroll
+                    for (int p = 0; p < NV / 32; ++p) {
+                        float z[32];
+                        if (c > 0) {
+                            tc::tmem_ld32(lane_base + kColS + 32 * p, z);
+                            tc::tmem_wait_ld();
+                        } else {
+                            load_init(p, z);
+                        }
+                        if (has_state && !states_only) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int ch = 4 * p + y;
+                                *reinterpret_cast<uint4 *>(row + (ch / 8) * (NK * 128) + (((ch & 7) ^ (d & 7)) << 4)) =
+                                    make_uint4(pack2(z[8 * y], z[8 * y + 1]), pack2(z[8 * y + 2], z[8 * y + 3]),
+                                               pack2(z[8 * y + 4], z[8 * y + 5]), pack2(z[8 * y + 6], z[8 * y + 7]));
+                            }
+                        }
+                        uint32_t out[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) out[j] = __float_as_uint(gn * z[j]);
+                        tc::tmem_st32(lane_base + kColS + 32 * p, out);
+                    }
+                    tc::tmem_wait_st();
+                }
+                tc::tc_fence_before();
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(bar(G::SReady));
+                ++cc;
+            }
+        }
+        if (!ok) *abort = 1;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+    if (tid == 0)
+        for (int i = blockIdx.x; i < a.nerr; i += gridDim.x) a.err[HB_IDX(i, a.nerr)] = i == (int)blockIdx.x ? *abort : 0;
+}
+
+// [B][L][heads][width] bf16 with rows `ld` elements apart; boxes of 64 entries x 1 head x 128 tokens
+bool make_map(CUtensorMap *m, const void *base, int B, int L, int heads, int width, long long ld) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)L, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * L};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)kC, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NK, int NV>
+cudaError_t launch(const Maps &m, const LinArgs &a, int items, bool states_only, cudaStream_t s) {
+    constexpr int smem = Geo<NK, NV>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = items < kLinMaxBlocks ? items : kLinMaxBlocks;
+    linattn_tc_kernel<NK, NV><<<grid, kThreads, smem, s>>>(m, a, items, states_only);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+HYENA_BOUNDS_READER(linattn_tc)
+
+bool linattn_tc_dims(int dtype, int dk, int dv) { return dtype == HYENA_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0; }
+
+// Segments: a chunk costs about 1, of the state pass 0.6 (no queries, no outputs); splitting adds two launches and
+// the passes over the segment states, about 4 chunks.
+LinPlan linattn_tc_plan(int B, int L, int Hk, int dv) {
+    LinPlan p{};
+    const int nv = dv <= 64 ? 64 : 128;
+    p.vtiles = (dv + nv - 1) / nv;
+    const double units = B > 0 ? (double)B * Hk * p.vtiles : 1.0;
+    const int chunks = L > 0 ? (L + kC - 1) / kC : 1;
+    auto waves = [](double x) { return (double)(long long)((x + kLinMaxBlocks - 1) / kLinMaxBlocks); };
+    double best = waves(units) * chunks;
+    int segc = chunks;
+    for (int want = 2; want <= chunks && want <= kLinMaxBlocks; ++want) {
+        const int sc = (chunks + want - 1) / want, ns = (chunks + sc - 1) / sc;
+        const double est = waves(units * ns) * sc + 0.6 * waves(units * (ns - 1)) * sc + 4.0;
+        if (est < best) { best = est; segc = sc; }
+    }
+    p.seg_tokens = segc * kC;
+    p.nseg = (chunks + segc - 1) / segc;
+    return p;
+}
+
+cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s) {
+    const long long items = (long long)(states_only ? a.nseg - 1 : a.nseg) * a.B * a.Hk * a.vtiles;
+    if (items > 0x7fffffffll - kLinMaxBlocks) return cudaErrorInvalidValue;
+    Maps m;
+    if (!make_map(&m.q, a.q, a.B, a.L, a.H, a.dk, a.ldq) || !make_map(&m.k, a.k, a.B, a.L, a.Hk, a.dk, a.ldk) ||
+        !make_map(&m.v, a.v, a.B, a.L, a.Hk, a.dv, a.ldv) || !make_map(&m.o, a.o, a.B, a.L, a.H, a.dv, (long long)a.H * a.dv))
+        return cudaErrorInvalidValue;
+    if (a.dk <= 64) return a.dv <= 64 ? launch<64, 64>(m, a, (int)items, states_only, s) : launch<64, 128>(m, a, (int)items, states_only, s);
+    return a.dv <= 64 ? launch<128, 64>(m, a, (int)items, states_only, s) : launch<128, 128>(m, a, (int)items, states_only, s);
+}
+
+}  // namespace hyena

@@ -61,6 +61,8 @@ SIGNATURES = {
     "hyena_fir_cache_prompt": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _fp, _vp]),
     "hyena_fir_decode_step": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _fp, _fp, _vp, _vp]),
     "hyena_linattn_prefill_workspace_bytes": (_sz, [_i] * 7),
+    "hyena_linattn_prefill_error_offset": (_sz, [_i] * 7),
+    "hyena_linattn_prefill_uses_tensor_cores": (_i, [_i] * 7 + [_ll] * 3 + [_vp] * 4),
     "hyena_linattn_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _fp, _vp, _fp,
                                    _vp, _sz, _vp]),
     "hyena_linattn_decode_step": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _vp, _i, _fp,
@@ -615,6 +617,26 @@ def linattn_prefill(q, k, v, decay, scale: float = 1.0, lens=None, state_in=None
                                            scale, _ptr(lens), _ptr(state_in), _ptr(o), _ptr(state), _ptr(workspace),
                                            workspace.numel(), _stream(dev)))
     return o, state
+
+
+def linattn_prefill_uses_tensor_cores(q, k, v, o=None) -> bool:
+    """Whether linattn_prefill with these tensors runs on the tensor cores (o None: a new one)."""
+    B, L, H, dk = q.shape
+    Hk, dv = v.shape[2:]
+    ld = [_rows(t, n, 4, q.dtype, q.device) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    st = lib().hyena_linattn_prefill_uses_tensor_cores(_act_dtype(q), B, L, H, Hk, dk, dv, *ld, _ptr(q), _ptr(k), _ptr(v),
+                                                      _ptr(o))
+    if st < 0:
+        _check("hyena_linattn_prefill_uses_tensor_cores", st)
+    return st == 1
+
+
+def linattn_error(workspace, dtype, B, L, H, Hk, dk, dv) -> int:
+    """The error words of linattn_prefill's tensor-core route (synchronises): 0 when every bounded wait
+    succeeded."""
+    lo = int(lib().hyena_linattn_prefill_error_offset(_DT[dtype], B, L, H, Hk, dk, dv))
+    hi = linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv)
+    return int(workspace[lo:hi].view(torch.int32).abs().max().item())
 
 
 def linattn_decode_step(q, k, v, decay, state, scale: float = 1.0, prep: QKPrep = None, positions=None, pos0: int = 0,

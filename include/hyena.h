@@ -272,7 +272,7 @@ int hyena_prefill_chunked_layers(int layers, const void *const *q, const void *c
  * one was, with record = {file, source line, index, extent} (file: 1 decode.cu,
  * 2 filter.cu, 3 fir.cu, 4 prefill_chunked.cu, 5 prefill_fft.cu, 6 state.cu,
  * 7 truncate.cu, 8 prefill_monarch.cu, 9 linattn.cu, 10 linattn_decode.cu,
- * 11 qk_norm.cu); HYENA_ERR_UNSUPPORTED from the release build, which has no
+ * 11 qk_norm.cu, 12 linattn_tc.cu); HYENA_ERR_UNSUPPORTED from the release build, which has no
  * checks; HYENA_ERR_ARG for a NULL record.
  */
 int hyena_debug_bounds_check(long long *record);
@@ -450,12 +450,29 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * 1 <= dk <= HYENA_MAX_HEAD_DIM, 1 <= dv, H dv and Hk dv < 2^31; B <= 65535.
  * Alignment: q, k, v, o to their element size, states 16 bytes (4 when dv is
  * not a multiple of 4), decay and lens 4.
- * Runs in fp32 on the CUDA cores.
+ * Routes.  bf16 activations with dk <= 128, dk and dv multiples of 8, row
+ * strides multiples of 8 elements and q, k, v, o 16-byte aligned run on the
+ * tensor cores: chunks of 128 tokens, o from bf16 products with fp32
+ * accumulation, the state in fp32 (its products take the weighted keys as sums
+ * of three bf16 terms, exact to fp32).  Every other call runs in fp32 on the CUDA
+ * cores.  hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the
+ * error that hyena_linattn_prefill would return); host-only.
+ * The tensor-core route waits on its own copies and products with bounded
+ * waits: the int32s from byte hyena_linattn_prefill_error_offset() to the end of
+ * the queried workspace are all 0 after a successful run of that route; another
+ * value means that a wait gave up and the outputs are not valid.  (The other
+ * route has no waits and leaves them as they were.)
+ * Values in q, k, v of a sequence's own tokens that are not finite may reach the
+ * outputs of tokens up to a chunk earlier, too.
  * Empty problems (B == 0, or L == 0) are valid; L == 0 writes state_out.
  */
 #define HYENA_MAX_HEAD_DIM 256
 
 size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
+size_t hyena_linattn_prefill_error_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv);
+int hyena_linattn_prefill_uses_tensor_cores(int dtype, int B, int L, int H, int Hk, int dk, int dv,
+                                            long long ldq, long long ldk, long long ldv,
+                                            const void *q, const void *k, const void *v, const void *o);
 int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype,
                           int B, int L, int H, int Hk, int dk, int dv,
                           long long ldq, long long ldk, long long ldv,

@@ -53,6 +53,22 @@ def test_prefill_workspace(lib):
     assert f(1, 1, 16, 3, 2, 8, 8) == 0 and f(5, 1, 16, 2, 2, 8, 8) == 0
 
 
+def test_route_query_and_error_words(lib):
+    f = lib.hyena_linattn_prefill_uses_tensor_cores
+
+    def route(dtype=1, dk=64, dv=64, ldq=256, ldk=128, ldv=128, q=FAKE, o=FAKE, H=4):
+        return f(dtype, 2, 16, H, 2, dk, dv, ldq, ldk, ldv, _p(q), _p(FAKE), _p(FAKE), _p(o))
+    assert route() == 1 and route(dk=8, dv=200, ldv=400) == 1 and route(ldq=264) == 1
+    for other in (dict(dtype=0), dict(dk=60), dict(dv=60), dict(dk=136, ldq=1000, ldk=1000), dict(ldq=260), dict(q=FAKE + 8),
+                  dict(o=FAKE + 2)):
+        assert route(**other) == 0, other
+    assert route(dtype=3) == ERR_ARG and route(H=3) == ERR_SHAPE and route(ldq=100) == ERR_SHAPE
+    for args in ((1, 2, 16, 4, 2, 64, 64), (1, 1, 65536, 12, 12, 64, 64), (0, 1, 300, 1, 1, 8, 8)):
+        off, n = lib.hyena_linattn_prefill_error_offset(*args), lib.hyena_linattn_prefill_workspace_bytes(*args)
+        assert off % 256 == 0 and (n - off) % 4 == 0 and n > off
+    assert lib.hyena_linattn_prefill_error_offset(1, 2, 16, 4, 3, 64, 64) == 0
+
+
 def decode(lib, dtype=1, B=2, H=4, Hk=2, dk=8, dv=8, ldq=None, q=FAKE, state=FAKE, prep=None, pos=0):
     return lib.hyena_linattn_decode_step(_p(q), _p(FAKE), _p(FAKE), dtype, B, H, Hk, dk, dv, H * dk if ldq is None else ldq, Hk * dk,
                                          Hk * dv, _p(FAKE), 1.0, prep, _p(pos), 0, _p(state), _p(FAKE), None)

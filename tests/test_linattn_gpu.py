@@ -44,18 +44,20 @@ def _run(B, L, H, Hk, dk, dv, dtype, *, lens=None, carry=False, fused=False, kin
             for t in (qd, kd, vd):
                 t[b, n:] = float("nan")
     o = torch.full((B, L, H, dv), 7.0, dtype=dtype, device="cuda")
-    o, st = ops.linattn_prefill(qd, kd, vd, dec, scale=scale, lens=ln, state_in=Sd, o=o)
+    dims = (dtype, B, L, H, Hk, dk, dv)
+    ws = torch.full((ops.linattn_prefill_workspace_bytes(*dims),), 255, dtype=torch.uint8, device="cuda")
+    o, st = ops.linattn_prefill(qd, kd, vd, dec, scale=scale, lens=ln, state_in=Sd, o=o, workspace=ws)
+    tc = ops.linattn_prefill_uses_tensor_cores(qd, kd, vd, o)
+    assert tc == (dtype == BF16 and dk <= 128 and dk % 8 == 0 and dv % 8 == 0)
+    if tc:
+        assert ops.linattn_error(ws, *dims) == 0, "a wait gave up"
     ref = reference(qd, kd, vd, dec, scale, ln, Sd)
     rows = None
     if lens is not None:
         rows = (torch.arange(L, device="cuda")[None] < ln[:, None])[..., None, None]
         assert bool((o.masked_select(~rows.expand_as(o)) == 7.0).all()), "rows behind a sequence were written"
-    check(o, st, ref, L, dk, dtype, _tc(qd, kd, vd, o), rows)
+    check(o, st, ref, L, dk, dtype, tc, rows)
     return qd, kd, vd, dec, Sd, o, st
-
-
-def _tc(q, k, v, o):
-    return False
 
 
 @pytest.mark.parametrize("L", [1, 2, 7, 8, 9, 63, 64, 65, 127, 128, 129, 300])
