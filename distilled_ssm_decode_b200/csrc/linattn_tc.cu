@@ -11,20 +11,21 @@
 //   scores  128 x 128 x dk   Q (shared) x K (shared)            -> columns kColP
 //   Q S     128 x dv x dk    Q (shared) x S as bf16 (shared)    -> columns kColO, then scaled in place
 //   P V     128 x dv x n     P as bf16 (tensor memory, over the scores) x V (shared), onto kColO
-//   state   dk x dv x n      weighted keys (tensor memory) x V (shared), onto the scaled state in kColS
+//   state   dk x dv x n      weighted keys (tensor memory) x V (shared), from zero -> kColU
 // Roundings to bf16: the scores' P and the state's copy that multiplies q (operands only; both reach o, itself bf16).
-// The state stays fp32 in tensor memory from chunk to chunk; its weighted keys are the sum of three bf16
-// terms (24 bits), so that it is as exact as an fp32 sum: one term would leave 2^-9, two 2^-17 of each token in a
-// state that every later token reads.
+// The state itself stays fp32, in registers; its weighted keys enter as the sum of three bf16 terms, which is
+// exact: one term would leave 2^-9, two 2^-17 of each token in a state that every later token reads.  A chunk's
+// contribution is summed from zero and joined by one fp32 multiply-add: summing onto the state in tensor memory
+// cut off (the units truncate) 24 times a chunk at the state's size, 1e-6 and more over a long prompt.
 //
 // Bound: 2 (dk + dv) (1 + 1) bytes per token and head of q, k, v, o against 2 C (dk + dv) + (2 + 6) dk dv operations:
 // memory-bound (at dk = dv = 128 the products need 55% of the time that the bytes need), if the chain
 // scores -> P -> P V -> o of a chunk overlaps the loads of the next and the state's own chain.  Hence one
 // persistent block per SM (a chunk's tiles fill shared memory) with a role for each warp group:
-//   warp 0 loads K, V; warp 1 loads Q; warp 2 issues every product; warp 3 stores O
+//   warp 0 loads K, V, Q; warp 1 stores O; warp 2 issues the products of the outputs, warp 3 those of the state
 //   warps 4-7   P group: a token row per thread: scores -> P, scaling of Q S, then O -> shared memory
 //   warps 8-11  K group: a row of the state (an entry of k) per thread: weighted keys -> tensor memory
-//   warps 12-15 S group: a row of the state per thread: the state's bf16 copy, its decay, its load and store
+//   warps 12-15 S group: a row of the state per thread, in registers: its decay and sum, its bf16 copy
 // They meet at mbarriers only.  Every wait is bounded; on timeout the block records it in its error word,
 // drains its copies and products, frees tensor memory and returns.
 //
@@ -44,10 +45,17 @@ namespace {
 constexpr int kC = 128;                 // tokens of a chunk
 constexpr int kThreads = 512;
 constexpr int kBlk = kC * 128;          // bytes of a [128 tokens][64 entries] bf16 tile, 128-byte swizzled
-constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColW = 384;   // tensor-memory columns
+constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColW = 384;   // tensor-memory columns
 constexpr uint32_t kTmemCols = 512;
 constexpr int kTerms = 3;               // bf16 terms of a weighted key
-constexpr int kHalf = 64;               // tokens of weighted keys held at a time: kTerms x 32 columns
+constexpr int kSub = 32;                // tokens of weighted keys in one of two buffers
+constexpr int kWBufs = 2, kWCols = kTerms * kSub / 2;
+static_assert(kColW + kWBufs * kWCols <= kTmemCols, "tensor memory");
+
+// Registers: the S group holds a row of the state in fp32.  The shares of the four warp groups add up to the
+// launch's 4 x 128 (checked before each launch: a larger sum would wait for ever).
+constexpr int kRegsLaunch = 128, kRegsMisc = 72, kRegsS = 184;
+static_assert(kRegsMisc + 2 * kRegsLaunch + kRegsS == 4 * kRegsLaunch, "register shares");
 
 struct Maps {
     CUtensorMap q, k, v, o;
@@ -58,21 +66,22 @@ struct Geo {
     static constexpr int kKB = NK / 64, kVB = NV / 64;                 // 64-entry blocks
     static constexpr int kStage = (kKB + kVB) * kBlk;                  // K, then V
     static constexpr int kQSlot = (kKB > kVB ? kKB : kVB) * kBlk;      // Q, then O
-    static constexpr int kStages = 2, kQSlots = 2;
+    static constexpr int kStages = NK + NV == 256 ? 2 : NK + NV == 192 ? 3 : 4, kQSlots = NK + NV == 128 ? 4 : 2;
     static constexpr int kSBytes = NK * NV * 2;
     static constexpr int kSmQ = kStages * kStage;
     static constexpr int kSmS = kSmQ + kQSlots * kQSlot;
     static constexpr int kSmPw = kSmS + kSBytes;                       // float pw[kC + 4], rev[32], rw[kC]
     static constexpr int kSmBar = kSmPw + 4 * (kC + 4 + 32 + kC);
     enum { KVFull = 0, KVEmpty = KVFull + kStages, QFull = KVEmpty + kStages, QEmpty = QFull + kQSlots,
-           OStaged = QEmpty + kQSlots, T1Done = OStaged + kQSlots, PReady, T2Done, OFree, WReady, WFree, SReady, SFree,
-           T3Done, Drain, kNumBars };
+           OStaged = QEmpty + kQSlots, T1Done = OStaged + kQSlots, QSDone, PReady, VReady, T2Done = VReady + kStages, OFree, WReady, WFree = WReady + kWBufs,
+           SReady = WFree + kWBufs, SFree, UDone, UFree, Drain, DrainU, kNumBars };
     static constexpr int kSmMisc = kSmBar + 8 * kNumBars;
     static constexpr int kSmem = kSmMisc + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kSmBar % 8 == 0 && kSmS % 1024 == 0, "alignment");
     __host__ __device__ static constexpr int count(int b) {
-        return (b >= OStaged && b < T1Done) || b == PReady || b == OFree || b == WReady || b == SReady ? 128 : 1;
+        return (b >= OStaged && b < T1Done) || b == PReady || (b >= VReady && b < T2Done) || b == OFree || (b >= WReady && b < WFree) || b == SReady ||
+                       b == UFree ? 128 : b >= KVEmpty && b < QFull ? 2 : 1;
     }
 };
 
@@ -80,7 +89,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
 }
-__device__ __forceinline__ float lo_of(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 struct Item {
@@ -100,6 +108,42 @@ __device__ __forceinline__ Item item_of(const LinArgs &a, int id, int nv) {
     it.ntok = min(len - it.t0, a.seg_tokens);
     it.nck = (it.ntok + kC - 1) / kC;
     return it;
+}
+
+// Weighted keys of kSub tokens for one entry of k (a thread's tensor-memory row): x = w k split into three bf16
+// terms by truncation -- an fp32 value has 24 significant bits, each term takes the leading 8 of what is left, so the
+// three add up to x exactly -- and stored two tokens to a column, term by term.  `ch` is the 16-byte piece of the
+// entry in its (swizzled) row; only the first n tokens count unless FULL.
+template <bool FULL>
+__device__ __forceinline__ void weigh(const uint8_t *col, int ch, const float *rw, int n, uint32_t cols) {
+    uint32_t t0[kSub / 2], t1[kSub / 2], t2[kSub / 2];
+#pragma unroll
+    for (int j = 0; j < kSub; j += 4) {
+        float w[4];
+        if (FULL) {
+            const float4 w4 = *reinterpret_cast<const float4 *>(rw + j);
+            w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
+        }
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = j + e;
+            const uint32_t kb = *reinterpret_cast<const uint16_t *>(col + t * 128 + ((ch ^ (t & 7)) << 4));
+            if (FULL) x[e] = __float_as_uint(__uint_as_float(kb << 16) * w[e]);
+            else x[e] = t < n ? __float_as_uint(__uint_as_float(kb << 16) * rw[t]) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const int i = (j + e) / 2;
+            t0[i] = __byte_perm(x[e], x[e + 1], 0x7632);
+            const float a = __uint_as_float(x[e]) - hi_of(x[e]), b = __uint_as_float(x[e + 1]) - hi_of(x[e + 1]);
+            t1[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+            t2[i] = __byte_perm(__float_as_uint(a - hi_of(__float_as_uint(a))), __float_as_uint(b - hi_of(__float_as_uint(b))), 0x7632);
+        }
+    }
+    tc::tmem_st16(cols, t0);
+    tc::tmem_st16(cols + kSub / 2, t1);
+    tc::tmem_st16(cols + kSub, t2);
 }
 
 template <int NK, int NV>
@@ -139,149 +183,171 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     const uint32_t tmem = (uint32_t)misc[1];
     auto uni = [&](bool x) -> bool { return __all_sync(0xffffffffu, x && !*abort); };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ K, V loads
-        if (lane == 0) {
-            int cc = 0;
-            bool ok = true;
-            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
-                const Item it = item_of(a, id, NV);
-                for (int c = 0; c < it.nck; ++c, ++cc) {
-                    const int st = cc % G::kStages;
-                    if (!(ok = tc::mbar_wait(bar(G::KVEmpty + st), ((cc / G::kStages) & 1) ^ 1, abort))) break;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
+        if (warp == 0) {
+            // ------------------------------------------------------------ loads
+            // K and V of the next chunk go out right behind the first queries of this one
+            if (lane == 0) {
+                int cc = 0, qc = 0, kv_id = blockIdx.x, kv_c = 0;
+                Item kv{};
+                if (kv_id < items) kv = item_of(a, kv_id, NV);
+                bool ok = true;
+                auto load_kv = [&]() {
+                    while (kv_id < items && kv_c >= kv.nck) {
+                        kv_id += gridDim.x;
+                        kv_c = 0;
+                        if (kv_id < items) kv = item_of(a, kv_id, NV);
+                    }
+                    if (kv_id >= items) return;
+                    const int st = cc % G::kStages, t = kv.t0 + kv_c * kC;
+                    if (!(ok = ok && tc::mbar_wait(bar(G::KVEmpty + st), ((cc / G::kStages) & 1) ^ 1, abort))) return;
                     const uint32_t dst = sbase + st * G::kStage;
                     tc::mbar_expect_tx(bar(G::KVFull + st), G::kStage);
-                    for (int x = 0; x < G::kKB; ++x)
-                        tc::tma_load_4d(dst + x * kBlk, &m.k, bar(G::KVFull + st), 64 * x, it.hk, it.t0 + c * kC, it.b);
+                    for (int x = 0; x < G::kKB; ++x) tc::tma_load_4d(dst + x * kBlk, &m.k, bar(G::KVFull + st), 64 * x, kv.hk, t, kv.b);
                     for (int x = 0; x < G::kVB; ++x)
-                        tc::tma_load_4d(dst + (G::kKB + x) * kBlk, &m.v, bar(G::KVFull + st), it.c0 + 64 * x, it.hk,
-                                        it.t0 + c * kC, it.b);
+                        tc::tma_load_4d(dst + (G::kKB + x) * kBlk, &m.v, bar(G::KVFull + st), kv.c0 + 64 * x, kv.hk, t, kv.b);
+                    ++cc;
+                    ++kv_c;
+                };
+                load_kv();
+                for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                    const Item it = item_of(a, id, NV);
+                    for (int c = 0; c < it.nck && ok; ++c) {
+                        for (int x = 0; x < Gq && ok && !states_only; ++x, ++qc) {
+                            const int s = qc % G::kQSlots;
+                            if (!(ok = tc::mbar_wait(bar(G::QEmpty + s), ((qc / G::kQSlots) & 1) ^ 1, abort))) break;
+                            tc::mbar_expect_tx(bar(G::QFull + s), G::kKB * kBlk);
+                            for (int y = 0; y < G::kKB; ++y)
+                                tc::tma_load_4d(sbase + G::kSmQ + s * G::kQSlot + y * kBlk, &m.q, bar(G::QFull + s), 64 * y,
+                                                it.hk * Gq + x, it.t0 + c * kC, it.b);
+                            if (x == 0) load_kv();
+                        }
+                        if (states_only) load_kv();
+                    }
+                }
+                if (!ok) {
+                    *abort = 1;
+                    for (int j = max(0, cc - G::kStages); j < cc; ++j)
+                        tc::mbar_wait(bar(G::KVFull + j % G::kStages), (j / G::kStages) & 1, never);
+                    for (int j = max(0, qc - G::kQSlots); j < qc; ++j)
+                        tc::mbar_wait(bar(G::QFull + j % G::kQSlots), (j / G::kQSlots) & 1, never);
                 }
             }
-            if (!ok) {
-                *abort = 1;
-                for (int j = max(0, cc - G::kStages); j < cc; ++j)
-                    tc::mbar_wait(bar(G::KVFull + j % G::kStages), (j / G::kStages) & 1, never);
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ Q loads
-        if (lane == 0 && !states_only) {
-            int qc = 0;
-            bool ok = true;
-            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
-                const Item it = item_of(a, id, NV);
-                for (int c = 0; c < it.nck && ok; ++c)
-                    for (int x = 0; x < Gq; ++x, ++qc) {
-                        const int s = qc % G::kQSlots;
-                        if (!(ok = tc::mbar_wait(bar(G::QEmpty + s), ((qc / G::kQSlots) & 1) ^ 1, abort))) break;
-                        tc::mbar_expect_tx(bar(G::QFull + s), G::kKB * kBlk);
-                        for (int y = 0; y < G::kKB; ++y)
-                            tc::tma_load_4d(sbase + G::kSmQ + s * G::kQSlot + y * kBlk, &m.q, bar(G::QFull + s), 64 * y,
-                                            it.hk * Gq + x, it.t0 + c * kC, it.b);
-                    }
-            }
-            if (!ok) {
-                *abort = 1;
-                for (int j = max(0, qc - G::kQSlots); j < qc; ++j)
-                    tc::mbar_wait(bar(G::QFull + j % G::kQSlots), (j / G::kQSlots) & 1, never);
-            }
-        }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ products
-        if (lane == 0) {
-            int cc = 0, qc = 0, wc = 0;
-            bool ok = true;
-            const uint32_t id_score = tc::idesc_bf16(128, 128, false), id_v = tc::idesc_bf16(128, NV, true);
-            auto wait = [&](int b, int phase) { return ok = ok && tc::mbar_wait(bar(b), phase & 1, abort); };
-            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
-                const Item it = item_of(a, id, NV);
-                for (int c = 0; c < it.nck && ok; ++c, ++cc) {
-                    const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
-                    const uint32_t k_at = sbase + st * G::kStage, v_at = k_at + G::kKB * kBlk;
-                    const bool has_state = c > 0 || (a.init && !states_only);
-                    if (!wait(G::KVFull + st, cc / G::kStages) || !wait(G::SReady, cc)) break;
-                    // state: the weighted keys of up to 64 tokens at a time
-                    auto state_product = [&]() {
-                        for (int h = 0; h * kHalf < n; ++h, ++wc) {
-                            if (!wait(G::WReady, wc)) return;
-                            tc::tc_fence_after();
-                            const int ks_end = min(kHalf / 16, steps - h * (kHalf / 16));
-                            for (int ks = 0; ks < ks_end; ++ks) {
-                                const uint64_t vd = tc::smem_desc_sw128(v_at + (h * (kHalf / 16) + ks) * 2048, kBlk, 1024);
-#pragma unroll
-                                for (int t = 0; t < kTerms; ++t)
-                                    tc::mma_bf16_ta(tmem + kColS, tmem + kColW + 32 * t + 8 * ks, vd, id_v, 1);
-                            }
-                            tc::mma_commit(bar(G::WFree));
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ O stores (whole chunks)
+            if (lane == 0 && !states_only) {
+                int qc = 0;
+                bool ok = true;
+                for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                    const Item it = item_of(a, id, NV);
+                    for (int c = 0; c < it.nck && ok; ++c)
+                        for (int x = 0; x < Gq; ++x, ++qc) {
+                            const int s = qc % G::kQSlots;
+                            if (!(ok = tc::mbar_wait(bar(G::OStaged + s), (qc / G::kQSlots) & 1, abort))) break;
+                            if (it.ntok - c * kC >= kC)
+                                for (int y = 0; y < G::kVB; ++y)
+                                    if (it.c0 + 64 * y < a.dv)
+                                        tc::tma_store_4d(&m.o, sbase + G::kSmQ + s * G::kQSlot + y * kBlk, it.c0 + 64 * y,
+                                                         it.hk * Gq + x, it.t0 + c * kC, it.b);
+                            tc::bulk_commit();
+                            tc::bulk_wait_read<0>();
+                            tc::mbar_arrive(bar(G::QEmpty + s));
                         }
-                        tc::mma_commit(bar(G::T3Done));
-                    };
-                    if (states_only) {
-                        state_product();
-                    } else {
-                        for (int x = 0; x < Gq && ok; ++x, ++qc) {
+                }
+                if (!ok) *abort = 1;
+                tc::bulk_wait<0>();
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ products of the outputs
+            if (lane == 0) {
+                int cc = 0, qc = 0;
+                bool ok = true;
+                const uint32_t id_score = tc::idesc_bf16(128, 128, false), id_v = tc::idesc_bf16(128, NV, true);
+                auto wait = [&](int b, int phase) { return ok = ok && tc::mbar_wait(bar(b), phase & 1, abort); };
+                for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                    const Item it = item_of(a, id, NV);
+                    for (int c = 0; c < it.nck && ok; ++c, ++cc) {
+                        const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
+                        const uint32_t k_at = sbase + st * G::kStage, v_at = k_at + G::kKB * kBlk;
+                        const bool has_state = c > 0 || a.init;
+                        if (!wait(G::KVFull + st, cc / G::kStages)) break;
+                        for (int x = 0; x < Gq && ok && !states_only; ++x, ++qc) {
                             const int s = qc % G::kQSlots;
                             if (!wait(G::QFull + s, qc / G::kQSlots) || !wait(G::OFree, qc + 1)) break;
                             tc::tc_fence_after();
                             const uint32_t q_at = sbase + G::kSmQ + s * G::kQSlot;
-#pragma unroll
+#pragma unroll 1
                             for (int ks = 0; ks < NK / 16; ++ks) {
                                 const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
                                 tc::mma_bf16(tmem + kColP, tc::smem_desc_sw128(q_at + off, 16, 1024),
                                              tc::smem_desc_sw128(k_at + off, 16, 1024), id_score, ks > 0);
                             }
+                            tc::mma_commit(bar(G::T1Done));
+                            if (x == 0 && !wait(G::SReady, cc)) break;
                             if (has_state) {
-#pragma unroll
+                                tc::tc_fence_after();
+#pragma unroll 1
                                 for (int ks = 0; ks < NK / 16; ++ks) {
                                     const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
                                     tc::mma_bf16(tmem + kColO, tc::smem_desc_sw128(q_at + off, 16, 1024),
                                                  tc::smem_desc_sw128(sbase + G::kSmS + ks * 2048, NK * 128, 1024), id_v, ks > 0);
                                 }
                             }
-                            tc::mma_commit(bar(G::T1Done));
+                            tc::mma_commit(bar(G::QSDone));
                             if (x == Gq - 1) tc::mma_commit(bar(G::SFree));
-                            if (x == 0) state_product();
-                            if (!wait(G::PReady, qc)) break;
+                            if (!wait(G::PReady, qc) || (x == 0 && !wait(G::VReady + st, cc / G::kStages))) break;
                             tc::tc_fence_after();
+#pragma unroll 1
                             for (int ks = 0; ks < steps; ++ks)
                                 tc::mma_bf16_ta(tmem + kColO, tmem + kColP + 8 * ks, tc::smem_desc_sw128(v_at + ks * 2048, kBlk, 1024),
                                                 id_v, has_state || ks > 0);
                             tc::mma_commit(bar(G::T2Done));
                         }
+                        tc::mma_commit(bar(G::KVEmpty + st));
                     }
-                    tc::mma_commit(bar(G::KVEmpty + st));
                 }
+                if (!ok) *abort = 1;
+                tc::mma_commit(bar(G::Drain));
+                tc::mbar_wait(bar(G::Drain), 0, never);
             }
-            if (!ok) *abort = 1;
-            tc::mma_commit(bar(G::Drain));
-            tc::mbar_wait(bar(G::Drain), 0, never);
-        }
-    } else if (warp == 3) {
-        // ------------------------------------------------------------ O stores (whole chunks)
-        if (lane == 0 && !states_only) {
-            int qc = 0, prev = -1;
-            bool ok = true;
-            for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
-                const Item it = item_of(a, id, NV);
-                for (int c = 0; c < it.nck && ok; ++c)
-                    for (int x = 0; x < Gq; ++x, ++qc) {
-                        const int s = qc % G::kQSlots;
-                        if (!(ok = tc::mbar_wait(bar(G::OStaged + s), (qc / G::kQSlots) & 1, abort))) break;
-                        if (it.ntok - c * kC >= kC)
-                            for (int y = 0; y < G::kVB; ++y)
-                                if (it.c0 + 64 * y < a.dv)
-                                    tc::tma_store_4d(&m.o, sbase + G::kSmQ + s * G::kQSlot + y * kBlk, it.c0 + 64 * y,
-                                                     it.hk * Gq + x, it.t0 + c * kC, it.b);
-                        tc::bulk_commit();
-                        tc::bulk_wait_read<0>();
-                        tc::mbar_arrive(bar(G::QEmpty + s));
-                        prev = s;
+        } else {
+            // ------------------------------------------------------------ products of the state
+            // the chunk's own contribution, from zero: kSub tokens of weighted keys at a time
+            if (lane == 0) {
+                int cc = 0, wc = 0;
+                bool ok = true;
+                const uint32_t id_v = tc::idesc_bf16(128, NV, true);
+                auto wait = [&](int b, int phase) { return ok = ok && tc::mbar_wait(bar(b), phase & 1, abort); };
+                for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
+                    const Item it = item_of(a, id, NV);
+                    for (int c = 0; c < it.nck && ok; ++c, ++cc) {
+                        const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
+                        const uint32_t v_at = sbase + st * G::kStage + G::kKB * kBlk;
+                        if (!wait(G::KVFull + st, cc / G::kStages) || !wait(G::UFree, cc + 1)) break;
+                        for (int h = 0; h * kSub < n; ++h, ++wc) {
+                            const int wb = wc % kWBufs;
+                            if (!wait(G::WReady + wb, wc / kWBufs)) break;
+                            tc::tc_fence_after();
+#pragma unroll 1
+                            for (int ks = 0; ks < min(kSub / 16, steps - h * (kSub / 16)); ++ks) {
+                                const uint64_t vd = tc::smem_desc_sw128(v_at + (h * (kSub / 16) + ks) * 2048, kBlk, 1024);
+#pragma unroll
+                                for (int t = 0; t < kTerms; ++t)
+                                    tc::mma_bf16_ta(tmem + kColU, tmem + kColW + wb * kWCols + (kSub / 2) * t + 8 * ks, vd, id_v,
+                                                    h > 0 || ks > 0 || t > 0);
+                            }
+                            tc::mma_commit(bar(G::WFree + wb));
+                        }
+                        if (!ok) break;
+                        tc::mma_commit(bar(G::UDone));
+                        tc::mma_commit(bar(G::KVEmpty + st));
                     }
+                }
+                if (!ok) *abort = 1;
+                tc::mma_commit(bar(G::DrainU));
+                tc::mbar_wait(bar(G::DrainU), 0, never);
             }
-            (void)prev;
-            if (!ok) *abort = 1;
-            tc::bulk_wait<0>();
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------ P group
@@ -337,7 +403,9 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         }
                         tc::tmem_st16(lane_base + kColP + 16 * p, out);
                     }
+                    if (!(ok = uni(tc::mbar_wait(bar(G::QSDone), qc & 1, abort)))) break;
                     if (has_state) {
+                        tc::tc_fence_after();
                         const float f = a.scale * pw[row + 1];
 #pragma unroll
                         for (int p = 0; p < NV / 32; ++p) {
@@ -400,58 +468,39 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
             for (int c = 0; c < it.nck && ok; ++c, ++cc) {
                 const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC);
                 if (!(ok = uni(tc::mbar_wait(bar(G::KVFull + st), (cc / G::kStages) & 1, abort)))) break;
-                uint8_t *kt = sm + st * G::kStage;
+                const uint8_t *kt = sm + st * G::kStage;
                 if (n & 15) {
                     // rows of V behind the last token, up to the products' step of 16: whatever they hold must not
                     // reach a sum
-                    uint8_t *vt = kt + G::kKB * kBlk;
+                    uint8_t *vt = sm + st * G::kStage + G::kKB * kBlk;
                     const int rows = 16 - (n & 15);
-                    for (int i = tid - 256; i < rows * 8 * G::kVB; i += 128)
+                    for (int i = d; i < rows * 8 * G::kVB; i += 128)
                         *reinterpret_cast<uint4 *>(vt + (i / (rows * 8)) * kBlk + (n + (i / 8) % rows) * 128 + (i & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     tc::fence_proxy_async_smem();
                 }
-                for (int h = 0; h * kHalf < n; ++h, ++wc) {
-                    if (!(ok = uni(tc::mbar_wait(bar(G::WFree), (wc & 1) ^ 1, abort)))) break;
+                tc::mbar_arrive(bar(G::VReady + st));
+                for (int h = 0; h * kSub < n; ++h, ++wc) {
+                    const int wb = wc % kWBufs;
+                    if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
                     tc::tc_fence_after();
                     if (32 * w < NK) {
-                        const uint8_t *col = kt + (d / 64) * kBlk + (d & 7) * 2;
+                        const uint32_t cols = lane_base + kColW + wb * kWCols;
+                        const uint8_t *col = kt + (d / 64) * kBlk + (d & 7) * 2 + h * (kSub * 128);
                         const int ch = (d & 63) >> 3;
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            uint32_t t0[16], t1[16], t2[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                float r[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int t = h * kHalf + 32 * y + 2 * j + e;
-                                    const uint16_t kb = *reinterpret_cast<const uint16_t *>(col + t * 128 + ((ch ^ (t & 7)) << 4));
-                                    // g^(n-1-t)
-                                    r[e] = t < n ? __uint_as_float((uint32_t)kb << 16) * rw[min(t + kC - n, kC - 1)] : 0.f;
-                                }
-                                t0[j] = pack2(r[0], r[1]);
-                                r[0] -= lo_of(t0[j]);
-                                r[1] -= hi_of(t0[j]);
-                                t1[j] = pack2(r[0], r[1]);
-                                r[0] -= lo_of(t1[j]);
-                                r[1] -= hi_of(t1[j]);
-                                t2[j] = pack2(r[0], r[1]);
-                            }
-                            tc::tmem_st16(lane_base + kColW + 16 * y, t0);
-                            tc::tmem_st16(lane_base + kColW + 32 + 16 * y, t1);
-                            tc::tmem_st16(lane_base + kColW + 64 + 16 * y, t2);
-                        }
+                        if (n == kC) weigh<true>(col, ch, rw + h * kSub, n - h * kSub, cols);
+                        else weigh<false>(col, ch, rw + kC - n + h * kSub, n - h * kSub, cols);
                         tc::tmem_wait_st();
                     }
                     tc::tc_fence_before();
-                    tc::mbar_arrive(bar(G::WReady));
+                    tc::mbar_arrive(bar(G::WReady + wb));
                 }
             }
         }
         if (!ok) *abort = 1;
     } else {
         // ------------------------------------------------------------ S group
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsS));
         const int w = warp & 3, d = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int cc = 0;
@@ -466,76 +515,50 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
             const float *init = states_only || !a.init ? nullptr : a.init + (long long)it.seg * a.init_stride;
             float *dst = states_only ? a.states + (long long)(it.seg + 1) * a.init_stride
                                      : it.seg == a.nseg - 1 ? a.state_out : nullptr;
-            auto load_init = [&](int p, float *z) {
+            float S[NV];                // this row of the state
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const int col = it.c0 + 32 * p + j;
-                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (init && d < a.dk && col < a.dv) t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + 32 * p + j, ns - 3));
-                    z[j] = t.x; z[j + 1] = t.y; z[j + 2] = t.z; z[j + 3] = t.w;
-                }
-            };
-            for (int c = 0; c <= it.nck && ok; ++c) {
-                // the state entering chunk c (or leaving the last one)
-                if (c > 0) {
-                    if (!(ok = uni(tc::mbar_wait(bar(G::T3Done), (cc - 1) & 1, abort)))) break;
-                    tc::tc_fence_after();
-                }
-                if (c == it.nck) {
-                    if (dst) {
+            for (int j = 0; j < NV; j += 4) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (init && d < a.dk && it.c0 + j < a.dv) t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + j, ns - 3));
+                S[j] = t.x; S[j + 1] = t.y; S[j + 2] = t.z; S[j + 3] = t.w;
+            }
+            for (int c = 0; c < it.nck; ++c, ++cc) {
+                if (!states_only) {
+                    // the copy that multiplies the queries, once every product with the last one is done
+                    if (!(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+                    if (32 * w < NK && (c > 0 || init)) {
+                        uint8_t *row = sm + G::kSmS + d * 128;
 #pragma unroll
-                        for (int p = 0; p < NV / 32; ++p) {
-                            float z[32];
-                            if (c > 0) {
-                                tc::tmem_ld32(lane_base + kColS + 32 * p, z);
-                                tc::tmem_wait_ld();
-                            } else {
-                                load_init(p, z);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                if (d < a.dk && it.c0 + 32 * p + j < a.dv && HB_OK(at + 32 * p + j + 3, ns))
-                                    *reinterpret_cast<float4 *>(dst + at + 32 * p + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
-                        }
+                        for (int ch = 0; ch < NV / 8; ++ch)
+                            *reinterpret_cast<uint4 *>(row + (ch / 8) * (NK * 128) + (((ch & 7) ^ (d & 7)) << 4)) =
+                                make_uint4(pack2(S[8 * ch], S[8 * ch + 1]), pack2(S[8 * ch + 2], S[8 * ch + 3]),
+                                           pack2(S[8 * ch + 4], S[8 * ch + 5]), pack2(S[8 * ch + 6], S[8 * ch + 7]));
+                        tc::fence_proxy_async_smem();
                     }
-                    tc::tc_fence_before();
-                    break;
+                    tc::mbar_arrive(bar(G::SReady));
                 }
-                const bool has_state = c > 0 || init;
-                // every product with the last chunk's copy is done
-                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+                if (!(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
+                tc::tc_fence_after();
                 const float gn = c == it.nck - 1 ? g_last : g_all;
                 if (32 * w < NK) {
-                    uint8_t *row = sm + G::kSmS + d * 128;
 #pragma unroll
-                    for (int p = 0; p < NV / 32; ++p) {
-                        float z[32];
-                        if (c > 0) {
-                            tc::tmem_ld32(lane_base + kColS + 32 * p, z);
-                            tc::tmem_wait_ld();
-                        } else {
-                            load_init(p, z);
-                        }
-                        if (has_state && !states_only) {
+                    for (int p = 0; p < NV / 16; ++p) {
+                        float z[16];
+                        tc::tmem_ld16(lane_base + kColU + 16 * p, z);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const int ch = 4 * p + y;
-                                *reinterpret_cast<uint4 *>(row + (ch / 8) * (NK * 128) + (((ch & 7) ^ (d & 7)) << 4)) =
-                                    make_uint4(pack2(z[8 * y], z[8 * y + 1]), pack2(z[8 * y + 2], z[8 * y + 3]),
-                                               pack2(z[8 * y + 4], z[8 * y + 5]), pack2(z[8 * y + 6], z[8 * y + 7]));
-                            }
-                        }
-                        uint32_t out[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) out[j] = __float_as_uint(gn * z[j]);
-                        tc::tmem_st32(lane_base + kColS + 32 * p, out);
+                        for (int j = 0; j < 16; ++j) S[16 * p + j] = fmaf(gn, S[16 * p + j], z[j]);
                     }
-                    tc::tmem_wait_st();
                 }
                 tc::tc_fence_before();
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(bar(G::SReady));
-                ++cc;
+                tc::mbar_arrive(bar(G::UFree));
+            }
+            if (!ok) break;
+            if (dst && d < a.dk) {
+#pragma unroll
+                for (int j = 0; j < NV; j += 4)
+                    if (it.c0 + j < a.dv && HB_OK(at + j + 3, ns))
+                        *reinterpret_cast<float4 *>(dst + at + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
         }
         if (!ok) *abort = 1;
@@ -572,6 +595,9 @@ cudaError_t launch(const Maps &m, const LinArgs &a, int items, bool states_only,
     constexpr int smem = Geo<NK, NV>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, linattn_tc_kernel<NK, NV>)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     const int grid = items < kLinMaxBlocks ? items : kLinMaxBlocks;
     linattn_tc_kernel<NK, NV><<<grid, kThreads, smem, s>>>(m, a, items, states_only);
     return cudaGetLastError();
