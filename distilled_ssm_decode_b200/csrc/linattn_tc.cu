@@ -81,7 +81,7 @@ struct Geo {
     static_assert(kSmBar % 8 == 0 && kSmS % 1024 == 0, "alignment");
     __host__ __device__ static constexpr int count(int b) {
         return (b >= OStaged && b < T1Done) || b == PReady || (b >= VReady && b < T2Done) || b == OFree || (b >= WReady && b < WFree) || b == SReady ||
-                       b == UFree ? 128 : b >= KVEmpty && b < QFull ? 2 : 1;
+                       b == UFree ? 4 : b >= KVEmpty && b < QFull ? 2 : 1;
     }
 };
 
@@ -182,6 +182,11 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     tc::tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[1];
     auto uni = [&](bool x) -> bool { return __all_sync(0xffffffffu, x && !*abort); };
+    // one arrival for each warp of a group (32 arrivals of a warp would be serialised)
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(b));
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
@@ -269,30 +274,33 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     const Item it = item_of(a, id, NV);
                     for (int c = 0; c < it.nck && ok; ++c, ++cc) {
                         const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
-                        const uint32_t k_at = sbase + st * G::kStage, v_at = k_at + G::kKB * kBlk;
+                        const uint32_t k_lo = tc::sw128_desc_lo(sbase + st * G::kStage, 16);
+                        const uint32_t v_lo = tc::sw128_desc_lo(sbase + st * G::kStage + G::kKB * kBlk, kBlk);
+                        const uint32_t s_lo = tc::sw128_desc_lo(sbase + G::kSmS, NK * 128);
                         const bool has_state = c > 0 || a.init;
                         if (!wait(G::KVFull + st, cc / G::kStages)) break;
                         for (int x = 0; x < Gq && ok && !states_only; ++x, ++qc) {
                             const int s = qc % G::kQSlots;
                             if (!wait(G::QFull + s, qc / G::kQSlots) || !wait(G::OFree, qc + 1)) break;
                             tc::tc_fence_after();
-                            const uint32_t q_at = sbase + G::kSmQ + s * G::kQSlot;
+                            const uint32_t q_lo = tc::sw128_desc_lo(sbase + G::kSmQ + s * G::kQSlot, 16);
 #pragma unroll 1
-                            for (int ks = 0; ks < NK / 16; ++ks) {
-                                const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
-                                tc::mma_bf16(tmem + kColP, tc::smem_desc_sw128(q_at + off, 16, 1024),
-                                             tc::smem_desc_sw128(k_at + off, 16, 1024), id_score, ks > 0);
-                            }
+                            for (int kb = 0; kb < G::kKB; ++kb)
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks) {
+                                    const uint32_t off = kb * (kBlk >> 4) + ks * 2;
+                                    tc::mma_bf16_sw128(tmem + kColP, q_lo + off, k_lo + off, id_score, kb + ks > 0);
+                                }
                             tc::mma_commit(bar(G::T1Done));
                             if (x == 0 && !wait(G::SReady, cc)) break;
                             if (has_state) {
                                 tc::tc_fence_after();
 #pragma unroll 1
-                                for (int ks = 0; ks < NK / 16; ++ks) {
-                                    const uint32_t off = (ks / 4) * kBlk + (ks % 4) * 32;
-                                    tc::mma_bf16(tmem + kColO, tc::smem_desc_sw128(q_at + off, 16, 1024),
-                                                 tc::smem_desc_sw128(sbase + G::kSmS + ks * 2048, NK * 128, 1024), id_v, ks > 0);
-                                }
+                                for (int kb = 0; kb < G::kKB; ++kb)
+#pragma unroll
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        tc::mma_bf16_sw128(tmem + kColO, q_lo + kb * (kBlk >> 4) + ks * 2,
+                                                           s_lo + (4 * kb + ks) * (2048 >> 4), id_v, kb + ks > 0);
                             }
                             tc::mma_commit(bar(G::QSDone));
                             if (x == Gq - 1) tc::mma_commit(bar(G::SFree));
@@ -300,8 +308,8 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                             tc::tc_fence_after();
 #pragma unroll 1
                             for (int ks = 0; ks < steps; ++ks)
-                                tc::mma_bf16_ta(tmem + kColO, tmem + kColP + 8 * ks, tc::smem_desc_sw128(v_at + ks * 2048, kBlk, 1024),
-                                                id_v, has_state || ks > 0);
+                                    tc::mma_bf16_ta_sw128(tmem + kColO, tmem + kColP + 8 * ks, v_lo + ks * (2048 >> 4), id_v,
+                                                          has_state || ks > 0);
                             tc::mma_commit(bar(G::T2Done));
                         }
                         tc::mma_commit(bar(G::KVEmpty + st));
@@ -323,20 +331,20 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     const Item it = item_of(a, id, NV);
                     for (int c = 0; c < it.nck && ok; ++c, ++cc) {
                         const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
-                        const uint32_t v_at = sbase + st * G::kStage + G::kKB * kBlk;
+                        const uint32_t v_lo = tc::sw128_desc_lo(sbase + st * G::kStage + G::kKB * kBlk, kBlk);
                         if (!wait(G::KVFull + st, cc / G::kStages) || !wait(G::UFree, cc + 1)) break;
                         for (int h = 0; h * kSub < n; ++h, ++wc) {
                             const int wb = wc % kWBufs;
                             if (!wait(G::WReady + wb, wc / kWBufs)) break;
                             tc::tc_fence_after();
-#pragma unroll 1
-                            for (int ks = 0; ks < min(kSub / 16, steps - h * (kSub / 16)); ++ks) {
-                                const uint64_t vd = tc::smem_desc_sw128(v_at + (h * (kSub / 16) + ks) * 2048, kBlk, 1024);
 #pragma unroll
-                                for (int t = 0; t < kTerms; ++t)
-                                    tc::mma_bf16_ta(tmem + kColU, tmem + kColW + wb * kWCols + (kSub / 2) * t + 8 * ks, vd, id_v,
-                                                    h > 0 || ks > 0 || t > 0);
-                            }
+                            for (int ks = 0; ks < kSub / 16; ++ks)
+                                if (h * (kSub / 16) + ks < steps)
+#pragma unroll
+                                    for (int t = 0; t < kTerms; ++t)
+                                        tc::mma_bf16_ta_sw128(tmem + kColU, tmem + kColW + wb * kWCols + (kSub / 2) * t + 8 * ks,
+                                                              v_lo + (h * (kSub / 16) + ks) * (2048 >> 4), id_v,
+                                                              h > 0 || ks > 0 || t > 0);
                             tc::mma_commit(bar(G::WFree + wb));
                         }
                         if (!ok) break;
@@ -354,6 +362,11 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int qc = 0, hk_cur = -1;
+        float f_row = 0.f;          // scale g^(i+1) of this row
+        // Decays of 0.6 and more: the sums are kept divided by the row's factor, O / (scale g^(i+1)), so that Q S needs no
+        // scaling and P's factor g^-(j+1) (at most 0.6^-128 < 2^95, far from overflow) depends on the column alone; the
+        // factor comes in with the output's rounding.  Smaller decays would overflow there: they scale Q S in place.
+        bool up = false;
         bool ok = !states_only;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
@@ -361,9 +374,10 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
             if (it.hk != hk_cur && it.nck > 0) {
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
-                pw[row] = (float)decay_pow(g, row);
-                if (row == 0) pw[kC] = (float)decay_pow(g, kC);
+                up = g >= 0.6;
+                pw[row] = (float)decay_pow(up ? 1.0 / g : g, up ? row + 1 : row);
                 if (row < 32) rev[row] = (float)decay_pow(g, 31 - row);
+                f_row = a.scale * (float)decay_pow(g, row + 1);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 hk_cur = it.hk;
             }
@@ -373,9 +387,8 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 for (int x = 0; x < Gq; ++x, ++qc) {
                     if (!(ok = uni(tc::mbar_wait(bar(G::T1Done), qc & 1, abort)))) break;
                     tc::tc_fence_after();
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        if (32 * p >= n) break;
+#pragma unroll 1
+                    for (int p = 0; 32 * p < n; ++p) {
                         uint32_t out[16];
                         if (p > w) {
 #pragma unroll
@@ -384,7 +397,19 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                             float z[32];
                             tc::tmem_ld32(lane_base + kColP + 32 * p, z);
                             tc::tmem_wait_ld();
-                            if (p < w) {
+                            if (up) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 4) {
+                                    const float4 r4 = *reinterpret_cast<const float4 *>(pw + 32 * p + j);
+                                    float y[4] = {z[j] * r4.x, z[j + 1] * r4.y, z[j + 2] * r4.z, z[j + 3] * r4.w};
+                                    if (p == w) {
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) y[e] = j + e <= lane ? y[e] : 0.f;
+                                    }
+                                    out[j / 2] = pack2(y[0], y[1]);
+                                    out[j / 2 + 1] = pack2(y[2], y[3]);
+                                }
+                            } else if (p < w) {
                                 const float f = a.scale * pw[row - (32 * p + 31)];
 #pragma unroll
                                 for (int j = 0; j < 32; j += 4) {
@@ -403,38 +428,39 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         }
                         tc::tmem_st16(lane_base + kColP + 16 * p, out);
                     }
-                    if (!(ok = uni(tc::mbar_wait(bar(G::QSDone), qc & 1, abort)))) break;
-                    if (has_state) {
+                    if (has_state && !up) {
+                        if (!(ok = uni(tc::mbar_wait(bar(G::QSDone), qc & 1, abort)))) break;
                         tc::tc_fence_after();
-                        const float f = a.scale * pw[row + 1];
-#pragma unroll
+#pragma unroll 1
                         for (int p = 0; p < NV / 32; ++p) {
                             float z[32];
                             tc::tmem_ld32(lane_base + kColO + 32 * p, z);
                             tc::tmem_wait_ld();
                             uint32_t out[32];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) out[j] = __float_as_uint(f * z[j]);
+                            for (int j = 0; j < 32; ++j) out[j] = __float_as_uint(f_row * z[j]);
                             tc::tmem_st32(lane_base + kColO + 32 * p, out);
                         }
                     }
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
-                    tc::mbar_arrive(bar(G::PReady));
+                    arrive(G::PReady);
                     if (!(ok = uni(tc::mbar_wait(bar(G::T2Done), qc & 1, abort)))) break;
                     tc::tc_fence_after();
                     const int s = qc % G::kQSlots;
                     uint8_t *ob = sm + G::kSmQ + s * G::kQSlot + row * 128;
+                    const float f = up ? f_row : 1.f;
                     const long long at = (((long long)it.b * a.L + it.t0 + c * kC + row) * a.H + it.hk * Gq + x) * a.dv + it.c0;
-#pragma unroll
+#pragma unroll 1
                     for (int p = 0; p < NV / 32; ++p) {
                         float z[32];
                         tc::tmem_ld32(lane_base + kColO + 32 * p, z);
                         tc::tmem_wait_ld();
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const uint4 v4 = make_uint4(pack2(z[8 * y], z[8 * y + 1]), pack2(z[8 * y + 2], z[8 * y + 3]),
-                                                        pack2(z[8 * y + 4], z[8 * y + 5]), pack2(z[8 * y + 6], z[8 * y + 7]));
+                            const float *t = z + 8 * y;
+                            const uint4 v4 = make_uint4(pack2(f * t[0], f * t[1]), pack2(f * t[2], f * t[3]),
+                                                        pack2(f * t[4], f * t[5]), pack2(f * t[6], f * t[7]));
                             const int ch = 4 * p + y;               // 16-byte piece of the row
                             if (n == kC)
                                 *reinterpret_cast<uint4 *>(ob + (ch / 8) * kBlk + (((ch & 7) ^ (row & 7)) << 4)) = v4;
@@ -444,9 +470,9 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         }
                     }
                     tc::tc_fence_before();
-                    tc::mbar_arrive(bar(G::OFree));
+                    arrive(G::OFree);
                     tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(bar(G::OStaged + s));
+                    arrive(G::OStaged + s);
                 }
             }
         }
@@ -479,7 +505,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                             make_uint4(0, 0, 0, 0);
                     tc::fence_proxy_async_smem();
                 }
-                tc::mbar_arrive(bar(G::VReady + st));
+                arrive(G::VReady + st);
                 for (int h = 0; h * kSub < n; ++h, ++wc) {
                     const int wb = wc % kWBufs;
                     if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
@@ -493,7 +519,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         tc::tmem_wait_st();
                     }
                     tc::tc_fence_before();
-                    tc::mbar_arrive(bar(G::WReady + wb));
+                    arrive(G::WReady + wb);
                 }
             }
         }
@@ -517,10 +543,37 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                                      : it.seg == a.nseg - 1 ? a.state_out : nullptr;
             float S[NV];                // this row of the state
 #pragma unroll
-            for (int j = 0; j < NV; j += 4) {
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (init && d < a.dk && it.c0 + j < a.dv) t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + j, ns - 3));
-                S[j] = t.x; S[j + 1] = t.y; S[j + 2] = t.z; S[j + 3] = t.w;
+            for (int j = 0; j < NV; ++j) S[j] = 0.f;
+            // Between global memory and the registers a warp's 32 rows pass through their own rows of the copy's room,
+            // half the columns at a time (16-byte pieces swizzled by row), so that global accesses are whole
+            // lines: a row per lane would cost one line per lane, and the other groups' shared-memory accesses
+            // would wait behind them.
+            constexpr int kPc = NV / 8;                  // 16-byte pieces of half a row
+            const bool mine = 32 * w < NK;
+            auto stage = [&](int r, int pc) {
+                return reinterpret_cast<float4 *>(sm + G::kSmS + (pc / 8) * (NK * 128) + (32 * w + r) * 128 + (((pc & 7) ^ (r & 7)) << 4));
+            };
+            if (init && mine) {
+                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int i = 0; i < kPc; ++i) {
+                        const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
+                        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (32 * w + r < a.dk && it.c0 + col < a.dv)
+                            t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + (long long)(r - lane) * a.dv + col, ns - 3));
+                        *stage(r, pc) = t;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int pc = 0; pc < kPc; ++pc) {
+                        const float4 t = *stage(lane, pc);
+                        const int j = hf * (NV / 2) + 4 * pc;
+                        S[j] = t.x; S[j + 1] = t.y; S[j + 2] = t.z; S[j + 3] = t.w;
+                    }
+                    __syncwarp();
+                }
             }
             for (int c = 0; c < it.nck; ++c, ++cc) {
                 if (!states_only) {
@@ -535,7 +588,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                                            pack2(S[8 * ch + 4], S[8 * ch + 5]), pack2(S[8 * ch + 6], S[8 * ch + 7]));
                         tc::fence_proxy_async_smem();
                     }
-                    tc::mbar_arrive(bar(G::SReady));
+                    arrive(G::SReady);
                 }
                 if (!(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
                 tc::tc_fence_after();
@@ -551,14 +604,27 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     }
                 }
                 tc::tc_fence_before();
-                tc::mbar_arrive(bar(G::UFree));
+                arrive(G::UFree);
             }
             if (!ok) break;
-            if (dst && d < a.dk) {
+            if (dst && mine) {
+                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
 #pragma unroll
-                for (int j = 0; j < NV; j += 4)
-                    if (it.c0 + j < a.dv && HB_OK(at + j + 3, ns))
-                        *reinterpret_cast<float4 *>(dst + at + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int pc = 0; pc < kPc; ++pc) {
+                        const int j = hf * (NV / 2) + 4 * pc;
+                        *stage(lane, pc) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kPc; ++i) {
+                        const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
+                        const long long x = at + (long long)(r - lane) * a.dv + col;
+                        if (32 * w + r < a.dk && it.c0 + col < a.dv && HB_OK(x + 3, ns)) *reinterpret_cast<float4 *>(dst + x) = *stage(r, pc);
+                    }
+                    __syncwarp();
+                }
             }
         }
         if (!ok) *abort = 1;
