@@ -35,6 +35,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "linattn.cuh"
 #include "tc.cuh"
 
@@ -659,11 +661,19 @@ bool make_map(CUtensorMap *m, const void *base, int B, int L, int heads, int wid
 template <int NK, int NV>
 cudaError_t launch(const Maps &m, const LinArgs &a, int items, bool states_only, cudaStream_t s) {
     constexpr int smem = Geo<NK, NV>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the kernel's attributes, once per device
+    static std::atomic<unsigned long long> ready{0};
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, linattn_tc_kernel<NK, NV>)) != cudaSuccess) return e;
-    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(linattn_tc_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, linattn_tc_kernel<NK, NV>)) != cudaSuccess) return e;
+        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
     const int grid = items < kLinMaxBlocks ? items : kLinMaxBlocks;
     linattn_tc_kernel<NK, NV><<<grid, kThreads, smem, s>>>(m, a, items, states_only);
     return cudaGetLastError();

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -474,6 +475,8 @@ def modal_truncate(lam, R, k: int):
 
 
 # ------------------------------------------------------------------ linear attention
+# A token's step takes a few microseconds on the GPU, so the host side of these calls is kept short: pointers go
+# to ctypes as plain integers, the stream is read as a number, sizes of workspaces are looked up.
 def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
     """Row stride (elements between consecutive tokens) of q, k or v [B][L][heads][width] (dim 4) or
     [B][heads][width] (dim 3): heads and width contiguous, rows evenly spaced, as a slice of one
@@ -484,42 +487,48 @@ def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions")
     sh, st = t.shape, t.stride()
-    width, n = sh[-1], sh[-2] * sh[-1]
-    if t.numel() == 0:
+    if len(sh) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    rows, heads, width = sh[0], sh[-2], sh[-1]
+    n = heads * width
+    if 0 in sh:
         return n
-    if (width > 1 and st[-1] != 1) or (sh[-2] > 1 and st[-2] != width):
+    if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if dim == 3:
-        ld = st[0] if sh[0] > 1 else n
-    elif sh[1] > 1:
-        ld = st[1]
-        if sh[0] > 1 and st[0] != sh[1] * ld:
-            raise ValueError(f"{name}: batch rows must follow each other at the token stride")
+    if dim == 3 or sh[1] == 1:
+        ld = st[0] if rows > 1 else n
     else:
-        ld = st[0] if sh[0] > 1 else n
+        ld = st[1]
+        if rows > 1 and st[0] != sh[1] * ld:
+            raise ValueError(f"{name}: batch rows must follow each other at the token stride")
     if ld < n:
         raise ValueError(f"{name}: tokens overlap")
     return ld
 
 
 def _plain(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this dtype, shape and device (None passes)."""
+    """The address of a contiguous tensor of this dtype, shape and device (None: None)."""
     if t is None:
         return None
     _cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t
+    return t.data_ptr()
 
 
-def _on(device):
-    """The library works on the current device: make it the tensors' one for a call."""
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+def _run(fn: str, device, *args):
+    """Call a library function on the current stream of `device` (the library works on the current device)."""
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if st != 0:
+        raise HyenaError(fn, st)
 
 
 class _CQKPrep(ctypes.Structure):
@@ -559,26 +568,30 @@ def qk_norm_rotate(q, k, prep: QKPrep, positions=None, pos0: int = 0, q_out=None
     pass.  positions int32 [B][L], or None: token t stands at pos0 + t.  q_out=q, k_out=k work in
     place.  Returns (q_out, k_out)."""
     dt, dev = _act_dtype(q), q.device
-    ldq, ldk = _rows(q, "q", 4, q.dtype, dev), _rows(k, "k", 4, q.dtype, dev)
+    dtype = q.dtype
+    ldq, ldk = _rows(q, "q", 4, dtype, dev), _rows(k, "k", 4, dtype, dev)
     B, L, H, hd = q.shape
-    Hk = k.shape[2]
-    if k.shape[:2] != q.shape[:2] or k.shape[3] != hd:
+    Bk, Lk, Hk, hk = k.shape
+    if Bk != B or Lk != L or hk != hd:
         raise ValueError("q and k must be [B][L][heads][hd] with the same B, L and hd")
-    _plain(positions, "positions", torch.int32, (B, L), dev)
+    pos = _plain(positions, "positions", torch.int32, (B, L), dev)
+    ldqo, ldko = H * hd, Hk * hd
     if q_out is None:
-        q_out = torch.empty((B, L, H, hd), dtype=q.dtype, device=dev)
+        q_out = q.new_empty((B, L, H, hd))
+    else:
+        ldqo = _rows(q_out, "q_out", 4, dtype, dev)
     if k_out is None:
-        k_out = torch.empty((B, L, Hk, hd), dtype=q.dtype, device=dev)
-    ldqo, ldko = _rows(q_out, "q_out", 4, q.dtype, dev), _rows(k_out, "k_out", 4, q.dtype, dev)
+        k_out = k.new_empty((B, L, Hk, hd))
+    else:
+        ldko = _rows(k_out, "k_out", 4, dtype, dev)
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out and k_out must have the shapes of q and k")
-    with _on(dev):
-        _check("hyena_qk_norm_rotate",
-               lib().hyena_qk_norm_rotate(_ptr(q), _ptr(k), dt, B, L, H, Hk, hd, ldq, ldk, prep._check(hd, dev),
-                                          _ptr(positions), pos0, _ptr(q_out), _ptr(k_out), ldqo, ldko, _stream(dev)))
+    _run("hyena_qk_norm_rotate", dev, q.data_ptr(), k.data_ptr(), dt, B, L, H, Hk, hd, ldq, ldk, prep._check(hd, dev),
+         pos, pos0, q_out.data_ptr(), k_out.data_ptr(), ldqo, ldko)
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=4096)
 def linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv) -> int:
     return int(lib().hyena_linattn_prefill_workspace_bytes(_DT[dtype], B, L, H, Hk, dk, dv))
 
@@ -591,31 +604,29 @@ def linattn_prefill(q, k, v, decay, scale: float = 1.0, lens=None, state_in=None
     [Hk], lens int32 [B] (tokens of each row; the rows of o behind them are left as they were, zero
     if o is made here), state_in float32 [B][Hk][dk][dv].  Returns (o [B][L][H][dv], state)."""
     dt, dev = _act_dtype(q), q.device
-    ldq, ldk, ldv = _rows(q, "q", 4, q.dtype, dev), _rows(k, "k", 4, q.dtype, dev), _rows(v, "v", 4, q.dtype, dev)
+    dtype = q.dtype
+    ldq, ldk, ldv = _rows(q, "q", 4, dtype, dev), _rows(k, "k", 4, dtype, dev), _rows(v, "v", 4, dtype, dev)
     B, L, H, dk = q.shape
-    Hk, dv = v.shape[2:]
-    if k.shape != (B, L, Hk, dk) or v.shape[:2] != (B, L):
+    Bv, Lv, Hk, dv = v.shape
+    if k.shape != (B, L, Hk, dk) or Bv != B or Lv != L:
         raise ValueError("q [B][L][H][dk], k [B][L][Hk][dk], v [B][L][Hk][dv] expected")
-    _plain(decay, "decay", torch.float32, (Hk,), dev)
-    _plain(lens, "lens", torch.int32, (B,), dev)
-    _plain(state_in, "state_in", torch.float32, (B, Hk, dk, dv), dev)
+    sshape = (B, Hk, dk, dv)
+    decay_at = _plain(decay, "decay", torch.float32, (Hk,), dev)
+    lens_at = _plain(lens, "lens", torch.int32, (B,), dev)
+    in_at = _plain(state_in, "state_in", torch.float32, sshape, dev)
     if o is None:
-        o = (torch.empty if lens is None else torch.zeros)((B, L, H, dv), dtype=q.dtype, device=dev)
+        o = (q.new_empty if lens is None else q.new_zeros)((B, L, H, dv))
     if state is None:
-        state = torch.empty((B, Hk, dk, dv), dtype=torch.float32, device=dev)
-    _plain(o, "o", q.dtype, (B, L, H, dv), dev)
-    _plain(state, "state", torch.float32, (B, Hk, dk, dv), dev)
-    with _on(dev):
-        if workspace is None:
-            nbytes = linattn_prefill_workspace_bytes(q.dtype, B, L, H, Hk, dk, dv)
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        _cuda(workspace, "workspace", torch.uint8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-        _check("hyena_linattn_prefill",
-               lib().hyena_linattn_prefill(_ptr(q), _ptr(k), _ptr(v), dt, B, L, H, Hk, dk, dv, ldq, ldk, ldv, _ptr(decay),
-                                           scale, _ptr(lens), _ptr(state_in), _ptr(o), _ptr(state), _ptr(workspace),
-                                           workspace.numel(), _stream(dev)))
+        state = q.new_empty(sshape, dtype=torch.float32)
+    o_at = _plain(o, "o", dtype, (B, L, H, dv), dev)
+    state_at = _plain(state, "state", torch.float32, sshape, dev)
+    if workspace is None:
+        workspace = q.new_empty(max(linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv), 1), dtype=torch.uint8)
+    _cuda(workspace, "workspace", torch.uint8)
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    _run("hyena_linattn_prefill", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, B, L, H, Hk, dk, dv, ldq, ldk, ldv,
+         decay_at, scale, lens_at, in_at, o_at, state_at, workspace.data_ptr(), workspace.numel())
     return o, state
 
 
@@ -647,22 +658,22 @@ def linattn_decode_step(q, k, v, decay, state, scale: float = 1.0, prep: QKPrep 
     through qk_norm_rotate's formulas in the same launch, at positions int32 [B] (None: pos0).
     Returns o [B][H][dv]."""
     dt, dev = _act_dtype(q), q.device
-    ldq, ldk, ldv = _rows(q, "q", 3, q.dtype, dev), _rows(k, "k", 3, q.dtype, dev), _rows(v, "v", 3, q.dtype, dev)
+    dtype = q.dtype
+    ldq, ldk, ldv = _rows(q, "q", 3, dtype, dev), _rows(k, "k", 3, dtype, dev), _rows(v, "v", 3, dtype, dev)
     B, H, dk = q.shape
-    Hk, dv = v.shape[1:]
-    if k.shape != (B, Hk, dk) or v.shape[0] != B:
+    Bv, Hk, dv = v.shape
+    if k.shape != (B, Hk, dk) or Bv != B:
         raise ValueError("q [B][H][dk], k [B][Hk][dk], v [B][Hk][dv] expected")
     if state is None:
         raise TypeError("state must be a CUDA tensor")
-    _plain(decay, "decay", torch.float32, (Hk,), dev)
-    _plain(state, "state", torch.float32, (B, Hk, dk, dv), dev)
-    _plain(positions, "positions", torch.int32, (B,), dev)
+    decay_at = _plain(decay, "decay", torch.float32, (Hk,), dev)
+    state_at = _plain(state, "state", torch.float32, (B, Hk, dk, dv), dev)
+    pos = _plain(positions, "positions", torch.int32, (B,), dev)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-    _plain(o, "o", q.dtype, (B, H, dv), dev)
-    with _on(dev):
-        _check("hyena_linattn_decode_step",
-               lib().hyena_linattn_decode_step(_ptr(q), _ptr(k), _ptr(v), dt, B, H, Hk, dk, dv, ldq, ldk, ldv, _ptr(decay),
-                                               scale, None if prep is None else prep._check(dk, dev), _ptr(positions),
-                                               pos0, _ptr(state), _ptr(o), _stream(dev)))
+        o = q.new_empty((B, H, dv))
+        o_at = o.data_ptr()
+    else:
+        o_at = _plain(o, "o", dtype, (B, H, dv), dev)
+    _run("hyena_linattn_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, B, H, Hk, dk, dv, ldq, ldk, ldv,
+         decay_at, scale, None if prep is None else prep._check(dk, dev), pos, pos0, state_at, o_at)
     return o
