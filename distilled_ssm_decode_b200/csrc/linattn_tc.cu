@@ -49,7 +49,11 @@ constexpr int kThreads = 512;
 constexpr int kBlk = kC * 128;          // bytes of a [128 tokens][64 entries] bf16 tile, 128-byte swizzled
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColW = 384;   // tensor-memory columns
 constexpr uint32_t kTmemCols = 512;
-constexpr int kTerms = 3;               // bf16 terms of a weighted key
+constexpr int kTerms = 4;               // bf16 terms of a weighted key
+// Decays of kUp and more: the sums are kept divided by the row's factor, O / (scale g^(i+1)), so that Q S needs no
+// scaling and P's factor g^-(j+1) (at most 0.75^-128 < 2^54) depends on the column alone; the row's factor comes in
+// with the output's rounding.  Smaller decays would overflow there: they scale P by rows and columns and Q S in place.
+constexpr double kUp = 0.75;
 constexpr int kSub = 32;                // tokens of weighted keys in one of two buffers
 constexpr int kWBufs = 2, kWCols = kTerms * kSub / 2;
 static_assert(kColW + kWBufs * kWCols <= kTmemCols, "tensor memory");
@@ -72,8 +76,8 @@ struct Geo {
     static constexpr int kSBytes = NK * NV * 2;
     static constexpr int kSmQ = kStages * kStage;
     static constexpr int kSmS = kSmQ + kQSlots * kQSlot;
-    static constexpr int kSmPw = kSmS + kSBytes;                       // float pw[kC + 4], rev[32], rw[kC]
-    static constexpr int kSmBar = kSmPw + 4 * (kC + 4 + 32 + kC);
+    static constexpr int kSmPw = kSmS + kSBytes;                       // float pw[kC], PairWeights rw[kC / 2]
+    static constexpr int kSmBar = kSmPw + 4 * kC + 16 * (kC / 2);
     enum { KVFull = 0, KVEmpty = KVFull + kStages, QFull = KVEmpty + kStages, QEmpty = QFull + kQSlots,
            OStaged = QEmpty + kQSlots, T1Done = OStaged + kQSlots, QSDone, PReady, VReady, T2Done = VReady + kStages, OFree, WReady, WFree = WReady + kWBufs,
            SReady = WFree + kWBufs, SFree, UDone, UFree, Drain, DrainU, kNumBars };
@@ -91,7 +95,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
 }
-__device__ __forceinline__ float hi_of(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 struct Item {
     int seg, b, hk, c0, t0, ntok, nck;      // first column, first token, tokens, chunks
@@ -112,40 +115,20 @@ __device__ __forceinline__ Item item_of(const LinArgs &a, int id, int nv) {
     return it;
 }
 
-// Weighted keys of kSub tokens for one entry of k (a thread's tensor-memory row): x = w k split into three bf16
-// terms by truncation -- an fp32 value has 24 significant bits, each term takes the leading 8 of what is left, so the
-// three add up to x exactly -- and stored two tokens to a column, term by term.  `ch` is the 16-byte piece of the
-// entry in its (swizzled) row; only the first n tokens count unless FULL.
-template <bool FULL>
-__device__ __forceinline__ void weigh(const uint8_t *col, int ch, const float *rw, int n, uint32_t cols) {
-    uint32_t t0[kSub / 2], t1[kSub / 2], t2[kSub / 2];
-#pragma unroll
-    for (int j = 0; j < kSub; j += 4) {
-        float w[4];
-        if (FULL) {
-            const float4 w4 = *reinterpret_cast<const float4 *>(rw + j);
-            w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
-        }
-        uint32_t x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = j + e;
-            const uint32_t kb = *reinterpret_cast<const uint16_t *>(col + t * 128 + ((ch ^ (t & 7)) << 4));
-            if (FULL) x[e] = __float_as_uint(__uint_as_float(kb << 16) * w[e]);
-            else x[e] = t < n ? __float_as_uint(__uint_as_float(kb << 16) * rw[t]) : 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const int i = (j + e) / 2;
-            t0[i] = __byte_perm(x[e], x[e + 1], 0x7632);
-            const float a = __uint_as_float(x[e]) - hi_of(x[e]), b = __uint_as_float(x[e + 1]) - hi_of(x[e + 1]);
-            t1[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-            t2[i] = __byte_perm(__float_as_uint(a - hi_of(__float_as_uint(a))), __float_as_uint(b - hi_of(__float_as_uint(b))), 0x7632);
-        }
-    }
-    tc::tmem_st16(cols, t0);
-    tc::tmem_st16(cols + kSub / 2, t1);
-    tc::tmem_st16(cols + kSub, t2);
+// w = w1 + w2 + w3 in bf16, for two tokens: |w - w1 - w2 - w3| <= 2^-27 |w|.
+struct __align__(16) PairWeights {
+    __nv_bfloat162 w1, w2, w3;
+    uint32_t pad;
+};
+__device__ __forceinline__ PairWeights split_weights(float a, float b) {
+    PairWeights p;
+    p.w1 = __floats2bfloat162_rn(a, b);
+    a -= __low2float(p.w1);
+    b -= __high2float(p.w1);
+    p.w2 = __floats2bfloat162_rn(a, b);
+    p.w3 = __floats2bfloat162_rn(a - __low2float(p.w2), b - __high2float(p.w2));
+    p.pad = 0;
+    return p;
 }
 
 template <int NK, int NV>
@@ -156,9 +139,8 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = tc::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float *pw = reinterpret_cast<float *>(sm + G::kSmPw);            // pw[n] = g^n
-    float *rev = pw + kC + 4;                                        // rev[x] = g^(31 - x)
-    float *rw = rev + 32;                                            // rw[x] = g^(kC - 1 - x) (the K group's)
+    float *pw = reinterpret_cast<float *>(sm + G::kSmPw);            // pw[x] = g^x, or g^-(x + 1) (the P group's)
+    PairWeights *rw = reinterpret_cast<PairWeights *>(pw + kC);      // rw[x]: g^(n - 1 - 2 x), g^(n - 2 - 2 x) (the K group's)
     volatile int *misc = reinterpret_cast<volatile int *>(sm + G::kSmMisc);   // abort (= error code), tensor memory, never
     volatile int *abort = misc, *never = misc + 2;
     auto bar = [&](int b) { return sbase + G::kSmBar + 8u * b; };
@@ -188,6 +170,38 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     auto arrive = [&](int b) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(b));
+    };
+
+    // one query tile's outputs: tensor memory -> bf16 -> shared memory (whole chunks, stored by warp 1) or o
+    auto outputs = [&](const Item &it, int c, int x, int qc, float f, int row, uint32_t lane_base) -> bool {
+        if (!uni(tc::mbar_wait(bar(G::T2Done), qc & 1, abort))) return false;
+        tc::tc_fence_after();
+        const int s = qc % G::kQSlots, n = min(kC, it.ntok - c * kC);
+        uint8_t *ob = sm + G::kSmQ + s * G::kQSlot + row * 128;
+        const long long at = (((long long)it.b * a.L + it.t0 + c * kC + row) * a.H + it.hk * Gq + x) * a.dv + it.c0;
+#pragma unroll 1
+        for (int p = 0; p < NV / 32; ++p) {
+            float z[32];
+            tc::tmem_ld32(lane_base + kColO + 32 * p, z);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float *t = z + 8 * y;
+                const uint4 v4 = make_uint4(pack2(f * t[0], f * t[1]), pack2(f * t[2], f * t[3]),
+                                            pack2(f * t[4], f * t[5]), pack2(f * t[6], f * t[7]));
+                const int ch = 4 * p + y;               // 16-byte piece of the row
+                if (n == kC)
+                    *reinterpret_cast<uint4 *>(ob + (ch / 8) * kBlk + (((ch & 7) ^ (row & 7)) << 4)) = v4;
+                else if (row < n && it.c0 + 8 * ch < a.dv &&
+                         HB_OK(at + 8 * ch + 7, (long long)a.B * a.L * a.H * a.dv))
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at + 8 * ch) = v4;
+            }
+        }
+        tc::tc_fence_before();
+        arrive(G::OFree);
+        tc::fence_proxy_async_smem();
+        arrive(G::OStaged + s);
+        return true;
     };
 
     if (warp < 4) {
@@ -267,54 +281,82 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
             }
         } else if (warp == 2) {
             // ------------------------------------------------------------ products of the outputs
+            // the scores of the next query tile go out as soon as P V of this one has read P, while the outputs are stored
             if (lane == 0) {
-                int cc = 0, qc = 0;
+                int cc = 0, qc = 0, sc = 0, id = blockIdx.x, c = 0, x = 0;
                 bool ok = true;
                 const uint32_t id_score = tc::idesc_bf16(128, 128, false), id_v = tc::idesc_bf16(128, NV, true);
+                const uint32_t s_lo = tc::sw128_desc_lo(sbase + G::kSmS, NK * 128);
                 auto wait = [&](int b, int phase) { return ok = ok && tc::mbar_wait(bar(b), phase & 1, abort); };
-                for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
-                    const Item it = item_of(a, id, NV);
-                    for (int c = 0; c < it.nck && ok; ++c, ++cc) {
-                        const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC), steps = (n + 15) / 16;
-                        const uint32_t k_lo = tc::sw128_desc_lo(sbase + st * G::kStage, 16);
-                        const uint32_t v_lo = tc::sw128_desc_lo(sbase + st * G::kStage + G::kKB * kBlk, kBlk);
-                        const uint32_t s_lo = tc::sw128_desc_lo(sbase + G::kSmS, NK * 128);
-                        const bool has_state = c > 0 || a.init;
-                        if (!wait(G::KVFull + st, cc / G::kStages)) break;
-                        for (int x = 0; x < Gq && ok && !states_only; ++x, ++qc) {
-                            const int s = qc % G::kQSlots;
-                            if (!wait(G::QFull + s, qc / G::kQSlots) || !wait(G::OFree, qc + 1)) break;
-                            tc::tc_fence_after();
-                            const uint32_t q_lo = tc::sw128_desc_lo(sbase + G::kSmQ + s * G::kQSlot, 16);
-#pragma unroll 1
-                            for (int kb = 0; kb < G::kKB; ++kb)
-#pragma unroll
-                                for (int ks = 0; ks < 4; ++ks) {
-                                    const uint32_t off = kb * (kBlk >> 4) + ks * 2;
-                                    tc::mma_bf16_sw128(tmem + kColP, q_lo + off, k_lo + off, id_score, kb + ks > 0);
-                                }
-                            tc::mma_commit(bar(G::T1Done));
-                            if (x == 0 && !wait(G::SReady, cc)) break;
-                            if (has_state) {
-                                tc::tc_fence_after();
-#pragma unroll 1
-                                for (int kb = 0; kb < G::kKB; ++kb)
-#pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        tc::mma_bf16_sw128(tmem + kColO, q_lo + kb * (kBlk >> 4) + ks * 2,
-                                                           s_lo + (4 * kb + ks) * (2048 >> 4), id_v, kb + ks > 0);
-                            }
-                            tc::mma_commit(bar(G::QSDone));
-                            if (x == Gq - 1) tc::mma_commit(bar(G::SFree));
-                            if (!wait(G::PReady, qc) || (x == 0 && !wait(G::VReady + st, cc / G::kStages))) break;
-                            tc::tc_fence_after();
-#pragma unroll 1
-                            for (int ks = 0; ks < steps; ++ks)
-                                    tc::mma_bf16_ta_sw128(tmem + kColO, tmem + kColP + 8 * ks, v_lo + ks * (2048 >> 4), id_v,
-                                                          has_state || ks > 0);
-                            tc::mma_commit(bar(G::T2Done));
+                Item it{};
+                auto settle = [&]() {
+                    for (; id < items; id += gridDim.x) {
+                        it = item_of(a, id, NV);
+                        if (it.nck > 0) return true;
+                    }
+                    return false;
+                };
+                auto q_at = [&]() { return tc::sw128_desc_lo(sbase + G::kSmQ + (qc % G::kQSlots) * G::kQSlot, 16); };
+                bool live = settle();
+                if (states_only) {
+                    for (; live && ok; ++cc) {           // the state's warp gives the stages back; this is its second arrival
+                        if (!wait(G::KVFull + cc % G::kStages, cc / G::kStages)) break;
+                        tc::mma_commit(bar(G::KVEmpty + cc % G::kStages));
+                        if (++c == it.nck) {
+                            c = 0;
+                            id += gridDim.x;
+                            live = settle();
                         }
+                    }
+                    live = false;
+                }
+                for (bool first = true; live && ok; first = false) {
+                    const int st = cc % G::kStages;
+                    if (!first && !wait(G::T2Done, qc - 1)) break;
+                    if ((x == 0 && !wait(G::KVFull + st, cc / G::kStages)) || !wait(G::QFull + qc % G::kQSlots, qc / G::kQSlots)) break;
+                    tc::tc_fence_after();
+                    const uint32_t q_lo = q_at(), k_lo = tc::sw128_desc_lo(sbase + st * G::kStage, 16);
+#pragma unroll 1
+                    for (int kb = 0; kb < G::kKB; ++kb)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = kb * (kBlk >> 4) + ks * 2;
+                            tc::mma_bf16_sw128(tmem + kColP, q_lo + off, k_lo + off, id_score, kb + ks > 0);
+                        }
+                    tc::mma_commit(bar(G::T1Done));
+                    const bool has_state = c > 0 || a.init;
+                    if (has_state && x == 0 && !wait(G::SReady, sc++)) break;
+                    if (!wait(G::OFree, qc + 1)) break;
+                    tc::tc_fence_after();
+                    if (has_state) {
+#pragma unroll 1
+                        for (int kb = 0; kb < G::kKB; ++kb)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc::mma_bf16_sw128(tmem + kColO, q_lo + kb * (kBlk >> 4) + ks * 2,
+                                                   s_lo + (4 * kb + ks) * (2048 >> 4), id_v, kb + ks > 0);
+                    }
+                    tc::mma_commit(bar(G::QSDone));
+                    if (has_state && x == Gq - 1) tc::mma_commit(bar(G::SFree));
+                    if (!wait(G::PReady, qc) || (x == 0 && !wait(G::VReady + st, cc / G::kStages))) break;
+                    tc::tc_fence_after();
+                    const uint32_t v_lo = tc::sw128_desc_lo(sbase + st * G::kStage + G::kKB * kBlk, kBlk);
+                    const int steps = (min(kC, it.ntok - c * kC) + 15) / 16;
+#pragma unroll 1
+                    for (int ks = 0; ks < steps; ++ks)
+                        tc::mma_bf16_ta_sw128(tmem + kColO, tmem + kColP + 8 * ks, v_lo + ks * (2048 >> 4), id_v,
+                                              has_state || ks > 0);
+                    tc::mma_commit(bar(G::T2Done));
+                    ++qc;
+                    if (++x == Gq) {
                         tc::mma_commit(bar(G::KVEmpty + st));
+                        x = 0;
+                        ++cc;
+                        if (++c == it.nck) {
+                            c = 0;
+                            id += gridDim.x;
+                            live = settle();
+                        }
                     }
                 }
                 if (!ok) *abort = 1;
@@ -365,20 +407,15 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int qc = 0, hk_cur = -1;
         float f_row = 0.f;          // scale g^(i+1) of this row
-        // Decays of 0.6 and more: the sums are kept divided by the row's factor, O / (scale g^(i+1)), so that Q S needs no
-        // scaling and P's factor g^-(j+1) (at most 0.6^-128 < 2^95, far from overflow) depends on the column alone; the
-        // factor comes in with the output's rounding.  Smaller decays would overflow there: they scale Q S in place.
-        bool up = false;
-        bool ok = !states_only;
+        bool up = false, ok = !states_only;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
             // the head's powers (this group writes its own table for itself)
             if (it.hk != hk_cur && it.nck > 0) {
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
-                up = g >= 0.6;
+                up = g >= kUp;
                 pw[row] = (float)decay_pow(up ? 1.0 / g : g, up ? row + 1 : row);
-                if (row < 32) rev[row] = (float)decay_pow(g, 31 - row);
                 f_row = a.scale * (float)decay_pow(g, row + 1);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 hk_cur = it.hk;
@@ -390,45 +427,40 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     if (!(ok = uni(tc::mbar_wait(bar(G::T1Done), qc & 1, abort)))) break;
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int p = 0; 32 * p < n; ++p) {
-                        uint32_t out[16];
-                        if (p > w) {
+                    for (int h = 0; 64 * h < n; ++h) {
+                        const int last = row - 64 * h;                    // the row's own token
+                        if (2 * h > w) {
+                            uint32_t none[32];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) out[j] = 0;      // later tokens
-                        } else {
-                            float z[32];
-                            tc::tmem_ld32(lane_base + kColP + 32 * p, z);
-                            tc::tmem_wait_ld();
+                            for (int j = 0; j < 32; ++j) none[j] = 0;     // later tokens
+                            tc::tmem_st32(lane_base + kColP + 32 * h, none);
+                            continue;
+                        }
+                        float z[64];
+                        tc::tmem_ld32(lane_base + kColP + 64 * h, z);
+                        tc::tmem_ld32(lane_base + kColP + 64 * h + 32, z + 32);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int p = 0; p < 64; p += 32) {
+                            uint32_t out[16];
                             if (up) {
 #pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 r4 = *reinterpret_cast<const float4 *>(pw + 32 * p + j);
-                                    float y[4] = {z[j] * r4.x, z[j + 1] * r4.y, z[j + 2] * r4.z, z[j + 3] * r4.w};
-                                    if (p == w) {
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) y[e] = j + e <= lane ? y[e] : 0.f;
-                                    }
-                                    out[j / 2] = pack2(y[0], y[1]);
-                                    out[j / 2 + 1] = pack2(y[2], y[3]);
-                                }
-                            } else if (p < w) {
-                                const float f = a.scale * pw[row - (32 * p + 31)];
-#pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 r4 = *reinterpret_cast<const float4 *>(rev + j);
-                                    out[j / 2] = pack2(z[j] * (f * r4.x), z[j + 1] * (f * r4.y));
-                                    out[j / 2 + 1] = pack2(z[j + 2] * (f * r4.z), z[j + 3] * (f * r4.w));
+                                for (int j = p; j < p + 32; j += 4) {
+                                    const float4 r4 = *reinterpret_cast<const float4 *>(pw + 64 * h + j);
+                                    z[j] *= r4.x; z[j + 1] *= r4.y; z[j + 2] *= r4.z; z[j + 3] *= r4.w;
                                 }
                             } else {
 #pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    const float y0 = j <= lane ? z[j] * (a.scale * pw[max(lane - j, 0)]) : 0.f;
-                                    const float y1 = j + 1 <= lane ? z[j + 1] * (a.scale * pw[max(lane - j - 1, 0)]) : 0.f;
-                                    out[j / 2] = pack2(y0, y1);
-                                }
+                                for (int j = p; j < p + 32; ++j) z[j] *= a.scale * pw[max(last - j, 0)];
                             }
+                            if (last < p + 31) {
+#pragma unroll
+                                for (int j = p; j < p + 32; ++j) z[j] = j <= last ? z[j] : 0.f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) out[j] = pack2(z[p + 2 * j], z[p + 2 * j + 1]);
+                            tc::tmem_st16(lane_base + kColP + 32 * h + p / 2, out);
                         }
-                        tc::tmem_st16(lane_base + kColP + 16 * p, out);
                     }
                     if (has_state && !up) {
                         if (!(ok = uni(tc::mbar_wait(bar(G::QSDone), qc & 1, abort)))) break;
@@ -447,34 +479,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     arrive(G::PReady);
-                    if (!(ok = uni(tc::mbar_wait(bar(G::T2Done), qc & 1, abort)))) break;
-                    tc::tc_fence_after();
-                    const int s = qc % G::kQSlots;
-                    uint8_t *ob = sm + G::kSmQ + s * G::kQSlot + row * 128;
-                    const float f = up ? f_row : 1.f;
-                    const long long at = (((long long)it.b * a.L + it.t0 + c * kC + row) * a.H + it.hk * Gq + x) * a.dv + it.c0;
-#pragma unroll 1
-                    for (int p = 0; p < NV / 32; ++p) {
-                        float z[32];
-                        tc::tmem_ld32(lane_base + kColO + 32 * p, z);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float *t = z + 8 * y;
-                            const uint4 v4 = make_uint4(pack2(f * t[0], f * t[1]), pack2(f * t[2], f * t[3]),
-                                                        pack2(f * t[4], f * t[5]), pack2(f * t[6], f * t[7]));
-                            const int ch = 4 * p + y;               // 16-byte piece of the row
-                            if (n == kC)
-                                *reinterpret_cast<uint4 *>(ob + (ch / 8) * kBlk + (((ch & 7) ^ (row & 7)) << 4)) = v4;
-                            else if (row < n && it.c0 + 8 * ch < a.dv &&
-                                     HB_OK(at + 8 * ch + 7, (long long)a.B * a.L * a.H * a.dv))
-                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at + 8 * ch) = v4;
-                        }
-                    }
-                    tc::tc_fence_before();
-                    arrive(G::OFree);
-                    tc::fence_proxy_async_smem();
-                    arrive(G::OStaged + s);
+                    if (!(ok = outputs(it, c, x, qc, up ? f_row : 1.f, row, lane_base))) break;
                 }
             }
         }
@@ -483,20 +488,24 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         // ------------------------------------------------------------ K group
         const int w = warp & 3, d = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-        int cc = 0, wc = 0, hk_cur = -1;
+        int cc = 0, wc = 0, hk_cur = -1, n_cur = 0;         // the table's head and chunk length
         bool ok = true;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
-            if (it.hk != hk_cur && it.nck > 0) {
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-                rw[d] = (float)decay_pow((double)a.decay[HB_IDX(it.hk, a.Hk)], kC - 1 - d);
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-                hk_cur = it.hk;
-            }
             for (int c = 0; c < it.nck && ok; ++c, ++cc) {
                 const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC);
+                if (it.hk != hk_cur || n != n_cur) {
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    if (d < kC / 2) {
+                        const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
+                        rw[d] = split_weights((float)decay_pow(g, max(n - 1 - 2 * d, 0)), (float)decay_pow(g, max(n - 2 - 2 * d, 0)));
+                    }
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    hk_cur = it.hk;
+                    n_cur = n;
+                }
                 if (!(ok = uni(tc::mbar_wait(bar(G::KVFull + st), (cc / G::kStages) & 1, abort)))) break;
-                const uint8_t *kt = sm + st * G::kStage;
+                const uint32_t kt = sbase + st * G::kStage;
                 if (n & 15) {
                     // rows of V behind the last token, up to the products' step of 16: whatever they hold must not
                     // reach a sum
@@ -512,12 +521,44 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     const int wb = wc % kWBufs;
                     if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
                     tc::tc_fence_after();
+                    // x = w k as four bf16 terms.  The product of two bf16 numbers is the sum of its rounding and
+                    // of what fma leaves, both exact: k w1 = t0 + e0, k w2 = t1 + e1; the last, k w3 + e1, is
+                    // rounded at 2^-26 |x|.  Two tokens to a column, the terms kSub / 2 columns apart.
                     if (32 * w < NK) {
-                        const uint32_t cols = lane_base + kColW + wb * kWCols;
-                        const uint8_t *col = kt + (d / 64) * kBlk + (d & 7) * 2 + h * (kSub * 128);
-                        const int ch = (d & 63) >> 3;
-                        if (n == kC) weigh<true>(col, ch, rw + h * kSub, n - h * kSub, cols);
-                        else weigh<false>(col, ch, rw + kC - n + h * kSub, n - h * kSub, cols);
+                        PairWeights pwt[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) pwt[m] = rw[h * (kSub / 2) + 4 * m + (lane & 3)];
+                        const uint32_t k_row = kt + (w / 2) * kBlk + (h * kSub + (lane >> 4) * 8 + (lane & 7)) * 128;
+#pragma unroll 1
+                        for (int hf = 0; hf < 2; ++hf) {              // 16 entries of k
+                            const int ch = (w & 1) * 4 + hf * 2 + ((lane >> 3) & 1);      // this lane's 16-byte piece of its row
+                            uint32_t x[8];
+                            tc::ldmatrix_x4_trans(k_row + ((ch ^ (lane & 7)) << 4), x);
+                            tc::ldmatrix_x4_trans(k_row + 16 * 128 + ((ch ^ (lane & 7)) << 4), x + 4);
+                            if (n != kC) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int t = h * kSub + (i / 2) * 8 + (lane & 3) * 2;
+                                    x[i] = t + 1 < n ? x[i] : t < n ? x[i] & 0xffffu : 0u;
+                                }
+                            }
+                            uint32_t t[kTerms][8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const PairWeights &p = pwt[i / 2];
+                                const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162 *>(&x[i]);
+                                const __nv_bfloat162 t0 = __hmul2_rn(k, p.w1), e0 = __hfma2(k, p.w1, __hneg2(t0));
+                                const __nv_bfloat162 t1 = __hmul2_rn(k, p.w2), e1 = __hfma2(k, p.w2, __hneg2(t1));
+                                const __nv_bfloat162 t2 = __hfma2(k, p.w3, e1);
+                                t[0][i] = *reinterpret_cast<const uint32_t *>(&t0);
+                                t[1][i] = *reinterpret_cast<const uint32_t *>(&e0);
+                                t[2][i] = *reinterpret_cast<const uint32_t *>(&t1);
+                                t[3][i] = *reinterpret_cast<const uint32_t *>(&t2);
+                            }
+                            const uint32_t cols = lane_base + ((uint32_t)(16 * hf) << 16) + kColW + wb * kWCols;
+#pragma unroll
+                            for (int y = 0; y < kTerms; ++y) tc::tmem_st_16x128b_x4(cols + y * (kSub / 2), t[y]);
+                        }
                         tc::tmem_wait_st();
                     }
                     tc::tc_fence_before();
@@ -531,7 +572,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsS));
         const int w = warp & 3, d = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-        int cc = 0;
+        int cc = 0, sc = 0;                              // chunks, copies of the state so far
         bool ok = true;
         const long long ns = (long long)a.B * a.Hk * a.dk * a.dv;
         (void)ns;
@@ -556,10 +597,10 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 return reinterpret_cast<float4 *>(sm + G::kSmS + (pc / 8) * (NK * 128) + (32 * w + r) * 128 + (((pc & 7) ^ (r & 7)) << 4));
             };
             if (init && mine) {
-                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
+#pragma unroll 4
                     for (int i = 0; i < kPc; ++i) {
                         const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
                         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -577,11 +618,31 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     __syncwarp();
                 }
             }
-            for (int c = 0; c < it.nck; ++c, ++cc) {
-                if (!states_only) {
+            // c = -1: only the copy of the entering state
+            for (int c = -1; c < it.nck; ++c) {
+                if (c >= 0) {
+                    if (!ok || !(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
+                    tc::tc_fence_after();
+                    const float gn = c == it.nck - 1 ? g_last : g_all;
+                    if (mine) {
+#pragma unroll
+                        for (int p = 0; p < NV / 16; ++p) {
+                            float z[16];
+                            tc::tmem_ld16(lane_base + kColU + 16 * p, z);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) S[16 * p + j] = fmaf(gn, S[16 * p + j], z[j]);
+                        }
+                    }
+                    tc::tc_fence_before();
+                    arrive(G::UFree);
+                    ++cc;
+                }
+                if (states_only) continue;
+                if (c + 1 < it.nck && (c >= 0 || init)) {
                     // the copy that multiplies the queries, once every product with the last one is done
-                    if (!(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
-                    if (32 * w < NK && (c > 0 || init)) {
+                    if (!(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
+                    if (mine) {
                         uint8_t *row = sm + G::kSmS + d * 128;
 #pragma unroll
                         for (int ch = 0; ch < NV / 8; ++ch)
@@ -591,26 +652,12 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         tc::fence_proxy_async_smem();
                     }
                     arrive(G::SReady);
+                    ++sc;
                 }
-                if (!(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
-                tc::tc_fence_after();
-                const float gn = c == it.nck - 1 ? g_last : g_all;
-                if (32 * w < NK) {
-#pragma unroll
-                    for (int p = 0; p < NV / 16; ++p) {
-                        float z[16];
-                        tc::tmem_ld16(lane_base + kColU + 16 * p, z);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) S[16 * p + j] = fmaf(gn, S[16 * p + j], z[j]);
-                    }
-                }
-                tc::tc_fence_before();
-                arrive(G::UFree);
             }
             if (!ok) break;
             if (dst && mine) {
-                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (cc & 1) ^ 1, abort)))) break;
+                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -619,7 +666,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         *stage(lane, pc) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
                     }
                     __syncwarp();
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < kPc; ++i) {
                         const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
                         const long long x = at + (long long)(r - lane) * a.dv + col;
