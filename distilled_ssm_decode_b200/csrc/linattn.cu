@@ -202,25 +202,41 @@ __global__ void __launch_bounds__(kThreads, RK <= 16 ? 2 : 1) linattn_kernel(con
 
 // The states entering the segments, in place over the segments' contributions: slot 0 becomes
 // state_in (or zero), slot s + 1 becomes g^(tokens of segment s) * slot s + its contribution.
-__global__ void __launch_bounds__(256) linattn_states_kernel(float *states, const float *state_in, long long n,
-                                                             long long per_head, int Hk, int L, int B, int nseg,
-                                                             int seg_tokens, const float *decay, const int *lens) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+// A thread carries V neighbouring entries through the segments, kAhead contributions in flight.
+constexpr int kStateThreads = 64, kAhead = 8;
+
+template <int V>
+__global__ void __launch_bounds__(kStateThreads) linattn_states_kernel(float *states, const float *state_in, long long n,
+                                                                       long long per_head, int Hk, int L, int B, int nseg,
+                                                                       int seg_tokens, const float *decay, const int *lens) {
+    struct alignas(4 * V) Vec { float x[V]; };
+    const long long i = ((long long)blockIdx.x * kStateThreads + threadIdx.x) * V;
     if (i >= n) return;
     const long long unit = i / per_head;
     const int hk = (int)(unit % Hk), b = (int)(unit / Hk);
     const double g = (double)decay[HB_IDX(hk, Hk)];
     const float whole = (float)decay_pow(g, seg_tokens);
     const int len = lens ? min(max(lens[HB_IDX(b, B)], 0), L) : L;
-    float x = state_in ? state_in[HB_IDX(i, n)] : 0.f;
-    if (HB_OK(i, n * nseg)) states[i] = x;
-    for (int s = 0; s + 1 < nseg; ++s) {
-        const int m = min(max(len - s * seg_tokens, 0), seg_tokens);
-        const float w = m == seg_tokens ? whole : (float)decay_pow(g, m);
-        const long long at = (s + 1) * n + i;
-        if (HB_OK(at, n * nseg)) {
-            x = fmaf(w, x, states[at]);
-            states[at] = x;
+    auto at = [&](int s) { return reinterpret_cast<Vec *>(states + HB_IDX(s * n + i + V - 1, n * nseg) - (V - 1)); };
+    Vec x;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x.x[v] = 0.f;
+    if (state_in) x = *reinterpret_cast<const Vec *>(state_in + HB_IDX(i, n - V + 1));
+    for (int s0 = 0; s0 + 1 < nseg; s0 += kAhead) {
+        Vec c[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (s0 + k + 1 < nseg) c[k] = *at(s0 + k + 1);
+        if (s0 == 0) *at(0) = x;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int s = s0 + k;
+            if (s + 1 >= nseg) break;
+            const int m = min(max(len - s * seg_tokens, 0), seg_tokens);
+            const float w = m == seg_tokens ? whole : (float)decay_pow(g, m);
+#pragma unroll
+            for (int v = 0; v < V; ++v) x.x[v] = fmaf(w, x.x[v], c[k].x[v]);
+            *at(s + 1) = x;
         }
     }
 }
@@ -300,10 +316,12 @@ cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, 
     if (p.nseg > 1) {
         cudaError_t e = run(true);
         if (e != cudaSuccess) return e;
-        const long long blocks = (a.init_stride + 255) / 256;
+        const int per = dv % 4 == 0 ? 4 * kStateThreads : kStateThreads;
+        const long long blocks = (a.init_stride + per - 1) / per;
         if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-        linattn_states_kernel<<<(unsigned)blocks, 256, 0, s>>>(a.states, state_in, a.init_stride, (long long)dk * dv, Hk, L,
-                                                               B, p.nseg, p.seg_tokens, decay, lens);
+        auto combine = dv % 4 == 0 ? linattn_states_kernel<4> : linattn_states_kernel<1>;
+        combine<<<(unsigned)blocks, kStateThreads, 0, s>>>(a.states, state_in, a.init_stride, (long long)dk * dv, Hk, L, B,
+                                                           p.nseg, p.seg_tokens, decay, lens);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         a.init = a.states;
     } else {

@@ -45,7 +45,7 @@ namespace hyena {
 namespace {
 
 constexpr int kC = 128;                 // tokens of a chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kBlk = kC * 128;          // bytes of a [128 tokens][64 entries] bf16 tile, 128-byte swizzled
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColW = 384;   // tensor-memory columns
 constexpr uint32_t kTmemCols = 512;
@@ -58,10 +58,10 @@ constexpr int kSub = 32;                // tokens of weighted keys in one of two
 constexpr int kWBufs = 2, kWCols = kTerms * kSub / 2;
 static_assert(kColW + kWBufs * kWCols <= kTmemCols, "tensor memory");
 
-// Registers: the S group holds a row of the state in fp32.  The shares of the four warp groups add up to the
-// launch's 4 x 128 (checked before each launch: a larger sum would wait for ever).
-constexpr int kRegsLaunch = 128, kRegsMisc = 72, kRegsS = 184;
-static_assert(kRegsMisc + 2 * kRegsLaunch + kRegsS == 4 * kRegsLaunch, "register shares");
+// Registers: the S groups hold half a row of the state in fp32.  The shares of the five warp groups must not exceed the
+// launch's 5 x 96 (checked before the first launch: a larger sum would wait for ever).
+constexpr int kRegsLaunch = 96, kRegsMisc = 56, kRegsS = 112;
+static_assert(kRegsMisc + 2 * kRegsLaunch + 2 * kRegsS <= 5 * kRegsLaunch, "register shares");
 
 struct Maps {
     CUtensorMap q, k, v, o;
@@ -69,7 +69,7 @@ struct Maps {
 
 template <int NK, int NV>
 struct Geo {
-    static constexpr int kKB = NK / 64, kVB = NV / 64;                 // 64-entry blocks
+    static constexpr int kKB = NK / 64, kVB = NV / 64, kNH = NV / 2;   // 64-entry blocks; columns of an S group
     static constexpr int kStage = (kKB + kVB) * kBlk;                  // K, then V
     static constexpr int kQSlot = (kKB > kVB ? kKB : kVB) * kBlk;      // Q, then O
     static constexpr int kStages = NK + NV == 256 ? 2 : NK + NV == 192 ? 3 : 4, kQSlots = NK + NV == 128 ? 4 : 2;
@@ -80,14 +80,15 @@ struct Geo {
     static constexpr int kSmBar = kSmPw + 4 * kC + 16 * (kC / 2);
     enum { KVFull = 0, KVEmpty = KVFull + kStages, QFull = KVEmpty + kStages, QEmpty = QFull + kQSlots,
            OStaged = QEmpty + kQSlots, T1Done = OStaged + kQSlots, QSDone, PReady, VReady, T2Done = VReady + kStages, OFree, WReady, WFree = WReady + kWBufs,
-           SReady = WFree + kWBufs, SFree, UDone, UFree, Drain, DrainU, kNumBars };
+           SReady = WFree + kWBufs, SFree, UDone, UFree, Drain, DrainU, PSync, KSync, SSync, kNumBars };
     static constexpr int kSmMisc = kSmBar + 8 * kNumBars;
     static constexpr int kSmem = kSmMisc + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kSmBar % 8 == 0 && kSmS % 1024 == 0, "alignment");
     __host__ __device__ static constexpr int count(int b) {
-        return (b >= OStaged && b < T1Done) || b == PReady || (b >= VReady && b < T2Done) || b == OFree || (b >= WReady && b < WFree) || b == SReady ||
-                       b == UFree ? 4 : b >= KVEmpty && b < QFull ? 2 : 1;
+        return b == SReady || b == UFree || b == SSync ? 8       // warps
+               : (b >= OStaged && b < T1Done) || b == OFree || b == PReady || (b >= VReady && b < T2Done) || (b >= WReady && b < WFree) || b == PSync || b == KSync ? 4
+               : b >= KVEmpty && b < QFull ? 2 : 1;
     }
 };
 
@@ -172,6 +173,11 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         if (lane == 0) tc::mbar_arrive(bar(b));
     };
 
+    // the warps of a group meet (bounded, as every wait here); `n` counts the meetings
+    auto meet = [&](int b, int &n) -> bool {
+        arrive(b);
+        return uni(tc::mbar_wait(bar(b), n++ & 1, abort));
+    };
     // one query tile's outputs: tensor memory -> bf16 -> shared memory (whole chunks, stored by warp 1) or o
     auto outputs = [&](const Item &it, int c, int x, int qc, float f, int row, uint32_t lane_base) -> bool {
         if (!uni(tc::mbar_wait(bar(G::T2Done), qc & 1, abort))) return false;
@@ -405,19 +411,19 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         // ------------------------------------------------------------ P group
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-        int qc = 0, hk_cur = -1;
+        int qc = 0, hk_cur = -1, met = 0;
         float f_row = 0.f;          // scale g^(i+1) of this row
         bool up = false, ok = !states_only;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
             // the head's powers (this group writes its own table for itself)
             if (it.hk != hk_cur && it.nck > 0) {
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (!(ok = meet(G::PSync, met))) break;
                 const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
                 up = g >= kUp;
                 pw[row] = (float)decay_pow(up ? 1.0 / g : g, up ? row + 1 : row);
                 f_row = a.scale * (float)decay_pow(g, row + 1);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (!(ok = meet(G::PSync, met))) break;
                 hk_cur = it.hk;
             }
             for (int c = 0; c < it.nck && ok; ++c) {
@@ -427,40 +433,33 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     if (!(ok = uni(tc::mbar_wait(bar(G::T1Done), qc & 1, abort)))) break;
                     tc::tc_fence_after();
 #pragma unroll 1
-                    for (int h = 0; 64 * h < n; ++h) {
-                        const int last = row - 64 * h;                    // the row's own token
-                        if (2 * h > w) {
-                            uint32_t none[32];
+                    for (int p = 0; 32 * p < n; ++p) {
+                        uint32_t out[16];
+                        if (p > w) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) none[j] = 0;     // later tokens
-                            tc::tmem_st32(lane_base + kColP + 32 * h, none);
-                            continue;
-                        }
-                        float z[64];
-                        tc::tmem_ld32(lane_base + kColP + 64 * h, z);
-                        tc::tmem_ld32(lane_base + kColP + 64 * h + 32, z + 32);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int p = 0; p < 64; p += 32) {
-                            uint32_t out[16];
+                            for (int j = 0; j < 16; ++j) out[j] = 0;      // later tokens
+                        } else {
+                            float z[32];
+                            tc::tmem_ld32(lane_base + kColP + 32 * p, z);
+                            tc::tmem_wait_ld();
                             if (up) {
 #pragma unroll
-                                for (int j = p; j < p + 32; j += 4) {
-                                    const float4 r4 = *reinterpret_cast<const float4 *>(pw + 64 * h + j);
+                                for (int j = 0; j < 32; j += 4) {
+                                    const float4 r4 = *reinterpret_cast<const float4 *>(pw + 32 * p + j);
                                     z[j] *= r4.x; z[j + 1] *= r4.y; z[j + 2] *= r4.z; z[j + 3] *= r4.w;
                                 }
                             } else {
 #pragma unroll
-                                for (int j = p; j < p + 32; ++j) z[j] *= a.scale * pw[max(last - j, 0)];
+                                for (int j = 0; j < 32; ++j) z[j] *= a.scale * pw[max(row - 32 * p - j, 0)];
                             }
-                            if (last < p + 31) {
+                            if (p == w) {
 #pragma unroll
-                                for (int j = p; j < p + 32; ++j) z[j] = j <= last ? z[j] : 0.f;
+                                for (int j = 0; j < 32; ++j) z[j] = j <= lane ? z[j] : 0.f;
                             }
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) out[j] = pack2(z[p + 2 * j], z[p + 2 * j + 1]);
-                            tc::tmem_st16(lane_base + kColP + 32 * h + p / 2, out);
+                            for (int j = 0; j < 16; ++j) out[j] = pack2(z[2 * j], z[2 * j + 1]);
                         }
+                        tc::tmem_st16(lane_base + kColP + 16 * p, out);
                     }
                     if (has_state && !up) {
                         if (!(ok = uni(tc::mbar_wait(bar(G::QSDone), qc & 1, abort)))) break;
@@ -488,19 +487,19 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         // ------------------------------------------------------------ K group
         const int w = warp & 3, d = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-        int cc = 0, wc = 0, hk_cur = -1, n_cur = 0;         // the table's head and chunk length
+        int cc = 0, wc = 0, hk_cur = -1, n_cur = 0, met = 0;         // the table's head and chunk length
         bool ok = true;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
             for (int c = 0; c < it.nck && ok; ++c, ++cc) {
                 const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC);
                 if (it.hk != hk_cur || n != n_cur) {
-                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    if (!(ok = meet(G::KSync, met))) break;
                     if (d < kC / 2) {
                         const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
                         rw[d] = split_weights((float)decay_pow(g, max(n - 1 - 2 * d, 0)), (float)decay_pow(g, max(n - 2 - 2 * d, 0)));
                     }
-                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                    if (!(ok = meet(G::KSync, met))) break;
                     hk_cur = it.hk;
                     n_cur = n;
                 }
@@ -568,67 +567,74 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         }
         if (!ok) *abort = 1;
     } else {
-        // ------------------------------------------------------------ S group
+        // ------------------------------------------------------------ S groups
+        // each has half of the columns of the state's rows, in registers
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsS));
-        const int w = warp & 3, d = 32 * w + lane;
+        constexpr int NH = G::kNH;
+        const int w = warp & 3, d = 32 * w + lane, sg = (warp - 12) >> 2;        // d: row of the state
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
-        int cc = 0, sc = 0;                              // chunks, copies of the state so far
+        int cc = 0, sc = 0, met = 0;                         // chunks, copies of the state so far
         bool ok = true;
         const long long ns = (long long)a.B * a.Hk * a.dk * a.dv;
-        (void)ns;
+        (void)ns; (void)met;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
             const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
             const float g_all = (float)decay_pow(g, kC), g_last = (float)decay_pow(g, it.ntok - (it.nck - 1) * kC);
-            const long long at = (((long long)it.b * a.Hk + it.hk) * a.dk + d) * a.dv + it.c0;
+            const int col0 = it.c0 + sg * NH;
+            const long long at = (((long long)it.b * a.Hk + it.hk) * a.dk + 32 * w) * a.dv + col0;       // this warp's rows
             const float *init = states_only || !a.init ? nullptr : a.init + (long long)it.seg * a.init_stride;
             float *dst = states_only ? a.states + (long long)(it.seg + 1) * a.init_stride
                                      : it.seg == a.nseg - 1 ? a.state_out : nullptr;
-            float S[NV];                // this row of the state
+            float S[NH];
 #pragma unroll
-            for (int j = 0; j < NV; ++j) S[j] = 0.f;
-            // Between global memory and the registers a warp's 32 rows pass through their own rows of the copy's room,
-            // half the columns at a time (16-byte pieces swizzled by row), so that global accesses are whole
-            // lines: a row per lane would cost one line per lane, and the other groups' shared-memory accesses
-            // would wait behind them.
-            constexpr int kPc = NV / 8;                  // 16-byte pieces of half a row
+            for (int j = 0; j < NH; ++j) S[j] = 0.f;
+            // Between global memory and the registers a warp's 32 rows pass through the copy's room, half of the group's
+            // columns at a time (16-byte pieces swizzled by row), so that global accesses are whole lines: a row per
+            // lane would cost one line per lane, and the other groups' shared-memory accesses would wait behind
+            // them.  With NV = 128 a row is staged where this thread copies it; with NV = 64 the rooms and the rows of
+            // the copy lie across one another, so all S warps meet in between.
+            constexpr int kPc = NH / 8;                      // 16-byte pieces of a staged row
             const bool mine = 32 * w < NK;
             auto stage = [&](int r, int pc) {
-                return reinterpret_cast<float4 *>(sm + G::kSmS + (pc / 8) * (NK * 128) + (32 * w + r) * 128 + (((pc & 7) ^ (r & 7)) << 4));
+                return reinterpret_cast<float4 *>(sm + G::kSmS + sg * (NK * NH * 2) + (32 * w + r) * (16 * kPc) + ((pc ^ (r & (kPc - 1))) << 4));
             };
-            if (init && mine) {
-                if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
+            if (init) {
+                if (!(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll 4
-                    for (int i = 0; i < kPc; ++i) {
-                        const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
-                        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (32 * w + r < a.dk && it.c0 + col < a.dv)
-                            t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + (long long)(r - lane) * a.dv + col, ns - 3));
-                        *stage(r, pc) = t;
-                    }
-                    __syncwarp();
+                    if (mine) {
 #pragma unroll
-                    for (int pc = 0; pc < kPc; ++pc) {
-                        const float4 t = *stage(lane, pc);
-                        const int j = hf * (NV / 2) + 4 * pc;
-                        S[j] = t.x; S[j + 1] = t.y; S[j + 2] = t.z; S[j + 3] = t.w;
+                        for (int i = 0; i < kPc; ++i) {
+                            const int r = (i * 32 + lane) / kPc, pc = lane % kPc, col = hf * (NH / 2) + 4 * pc;
+                            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (32 * w + r < a.dk && col0 + col < a.dv)
+                                t = *reinterpret_cast<const float4 *>(init + HB_IDX(at + (long long)r * a.dv + col, ns - 3));
+                            *stage(r, pc) = t;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int pc = 0; pc < kPc; ++pc) {
+                            const float4 t = *stage(lane, pc);
+                            const int j = hf * (NH / 2) + 4 * pc;
+                            S[j] = t.x; S[j + 1] = t.y; S[j + 2] = t.z; S[j + 3] = t.w;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                if (NV == 64 && !(ok = meet(G::SSync, met))) break;
             }
             // c = -1: only the copy of the entering state
             for (int c = -1; c < it.nck; ++c) {
                 if (c >= 0) {
-                    if (!ok || !(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
+                    if (!(ok = uni(tc::mbar_wait(bar(G::UDone), cc & 1, abort)))) break;
                     tc::tc_fence_after();
                     const float gn = c == it.nck - 1 ? g_last : g_all;
                     if (mine) {
 #pragma unroll
-                        for (int p = 0; p < NV / 16; ++p) {
+                        for (int p = 0; p < NH / 16; ++p) {
                             float z[16];
-                            tc::tmem_ld16(lane_base + kColU + 16 * p, z);
+                            tc::tmem_ld16(lane_base + kColU + sg * NH + 16 * p, z);
                             tc::tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j) S[16 * p + j] = fmaf(gn, S[16 * p + j], z[j]);
@@ -645,10 +651,12 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     if (mine) {
                         uint8_t *row = sm + G::kSmS + d * 128;
 #pragma unroll
-                        for (int ch = 0; ch < NV / 8; ++ch)
+                        for (int i = 0; i < NH / 8; ++i) {
+                            const int ch = sg * (NH / 8) + i;
                             *reinterpret_cast<uint4 *>(row + (ch / 8) * (NK * 128) + (((ch & 7) ^ (d & 7)) << 4)) =
-                                make_uint4(pack2(S[8 * ch], S[8 * ch + 1]), pack2(S[8 * ch + 2], S[8 * ch + 3]),
-                                           pack2(S[8 * ch + 4], S[8 * ch + 5]), pack2(S[8 * ch + 6], S[8 * ch + 7]));
+                                make_uint4(pack2(S[8 * i], S[8 * i + 1]), pack2(S[8 * i + 2], S[8 * i + 3]),
+                                           pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
+                        }
                         tc::fence_proxy_async_smem();
                     }
                     arrive(G::SReady);
@@ -656,24 +664,27 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 }
             }
             if (!ok) break;
-            if (dst && mine) {
+            if (dst) {
                 if (!states_only && !(ok = uni(tc::mbar_wait(bar(G::SFree), (sc & 1) ^ 1, abort)))) break;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
+                    if (mine) {
 #pragma unroll
-                    for (int pc = 0; pc < kPc; ++pc) {
-                        const int j = hf * (NV / 2) + 4 * pc;
-                        *stage(lane, pc) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-                    }
-                    __syncwarp();
+                        for (int pc = 0; pc < kPc; ++pc) {
+                            const int j = hf * (NH / 2) + 4 * pc;
+                            *stage(lane, pc) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                        }
+                        __syncwarp();
 #pragma unroll 2
-                    for (int i = 0; i < kPc; ++i) {
-                        const int r = (i * 32 + lane) / kPc, pc = (i * 32 + lane) % kPc, col = hf * (NV / 2) + 4 * pc;
-                        const long long x = at + (long long)(r - lane) * a.dv + col;
-                        if (32 * w + r < a.dk && it.c0 + col < a.dv && HB_OK(x + 3, ns)) *reinterpret_cast<float4 *>(dst + x) = *stage(r, pc);
+                        for (int i = 0; i < kPc; ++i) {
+                            const int r = (i * 32 + lane) / kPc, pc = lane % kPc, col = hf * (NH / 2) + 4 * pc;
+                            const long long x = at + (long long)r * a.dv + col;
+                            if (32 * w + r < a.dk && col0 + col < a.dv && HB_OK(x + 3, ns)) *reinterpret_cast<float4 *>(dst + x) = *stage(r, pc);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                if (NV == 64 && !states_only && !(ok = meet(G::SSync, met))) break;
             }
         }
         if (!ok) *abort = 1;
