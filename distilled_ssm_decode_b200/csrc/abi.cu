@@ -479,12 +479,12 @@ static int check_prep(const hyena_qk_prep *p, int hd) {
 
 size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
     if (check_linattn(dtype, B, L, H, Hk, dk, dv) != HYENA_OK) return 0;
-    return linattn_ws_bytes(dtype, B, L, Hk, dk, dv);
+    return linattn_ws_bytes(dtype, B, L, H, Hk, dk, dv);
 }
 
 size_t hyena_linattn_prefill_error_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
     if (check_linattn(dtype, B, L, H, Hk, dk, dv) != HYENA_OK) return 0;
-    return linattn_err_offset(dtype, B, L, Hk, dk, dv);
+    return linattn_err_offset(dtype, B, L, H, Hk, dk, dv);
 }
 
 int hyena_linattn_prefill_uses_tensor_cores(int dtype, int B, int L, int H, int Hk, int dk, int dv, long long ldq,
@@ -519,7 +519,7 @@ int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype
     const size_t ab = (dtype == HYENA_BF16) ? 2 : 4;
     if (!aligned(q, ab) || !aligned(k, ab) || !aligned(v, ab) || !aligned(o, ab) || !aligned(workspace, kAlign))
         return HYENA_ERR_ALIGN;
-    if (ws_bytes < linattn_ws_bytes(dtype, B, L, Hk, dk, dv)) return HYENA_ERR_WORKSPACE;
+    if (ws_bytes < linattn_ws_bytes(dtype, B, L, H, Hk, dk, dv)) return HYENA_ERR_WORKSPACE;
     HYENA_LAUNCH_GUARD();
     return cuda_status(launch_linattn_prefill(q, k, v, dtype, B, L, H, Hk, dk, dv, ldq, ldk, ldv, decay, scale, lens,
                                               state_in, o, state_out, workspace, s));

@@ -280,14 +280,15 @@ bool linattn_uses_tc(int dtype, int dk, int dv, long long ldq, long long ldk, lo
 
 // Workspace: [segment states][error words of the state pass][error words of the main pass].  The queries know
 // neither strides nor pointers, so there is room for whichever route is taken.
-size_t linattn_err_offset(int dtype, int B, int L, int Hk, int dk, int dv) {
+size_t linattn_err_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
     int nseg = simt_plan(B, L, Hk, dv).nseg;
-    if (linattn_tc_dims(dtype, dk, dv)) nseg = max(nseg, linattn_tc_plan(B, L, Hk, dv).nseg);
+    if (linattn_tc_dims(dtype, dk, dv))
+        nseg = max(nseg, max(linattn_tc_plan(B, L, H, Hk, dk, dv, false).nseg, linattn_tc_plan(B, L, H, Hk, dk, dv, true).nseg));
     return al256(nseg > 1 ? (size_t)nseg * B * Hk * dk * dv * sizeof(float) : 0);
 }
 
-size_t linattn_ws_bytes(int dtype, int B, int L, int Hk, int dk, int dv) {
-    return linattn_err_offset(dtype, B, L, Hk, dk, dv) + 2 * kLinMaxBlocks * sizeof(int);
+size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
+    return linattn_err_offset(dtype, B, L, H, Hk, dk, dv) + 2 * kLinMaxBlocks * sizeof(int);
 }
 
 cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk,
@@ -295,17 +296,17 @@ cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, 
                                    float scale, const int *lens, const float *state_in, void *o, float *state_out,
                                    void *ws, cudaStream_t s) {
     const bool tc = linattn_uses_tc(dtype, dk, dv, ldq, ldk, ldv, q, k, v, o);
-    const LinPlan p = tc ? linattn_tc_plan(B, L, Hk, dv) : simt_plan(B, L, Hk, dv);
+    const LinPlan p = tc ? linattn_tc_plan(B, L, H, Hk, dk, dv, lens != nullptr) : simt_plan(B, L, Hk, dv);
     LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.o = o;
     a.B = B; a.L = L; a.H = H; a.Hk = Hk; a.dk = dk; a.dv = dv;
     a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
     a.decay = decay; a.scale = scale; a.lens = lens;
     a.state_out = state_out;
-    a.seg_tokens = p.seg_tokens; a.nseg = p.nseg; a.vtiles = p.vtiles;
+    a.seg_tokens = p.seg_tokens; a.nseg = p.nseg; a.vtiles = p.vtiles; a.nv = p.nv;
     a.init_stride = (long long)B * Hk * dk * dv;
     a.states = static_cast<float *>(ws);
-    int *err = reinterpret_cast<int *>(static_cast<char *>(ws) + linattn_err_offset(dtype, B, L, Hk, dk, dv));
+    int *err = reinterpret_cast<int *>(static_cast<char *>(ws) + linattn_err_offset(dtype, B, L, H, Hk, dk, dv));
     auto run = [&](bool states_only) {
         // both sets of words are written when there is no state pass
         a.err = states_only || p.nseg == 1 ? err : err + kLinMaxBlocks;

@@ -30,7 +30,7 @@ struct LinArgs {
     float *states;           // states_only: contribution of segment s -> states + (s + 1) * init_stride
     float *state_out;        // else: the state after the last segment
     int seg_tokens, nseg;    // segments of this launch (states_only leaves out the last one)
-    int vtiles;              // column tiles of a state
+    int vtiles, nv;          // column tiles of a state, their width
     int *err;                // tensor-core route: an error word for each block
     int nerr;
 };
@@ -45,13 +45,13 @@ __device__ __forceinline__ int row_tokens(const LinArgs &a, int b) {
 // column tile) units to fill the GPU: the segments' own contributions to the state are computed
 // first, then combined into the state entering each segment, then every segment runs by itself.
 struct LinPlan {
-    int vtiles, nseg, seg_tokens;
+    int vtiles, nv, nseg, seg_tokens;
 };
 
 // linattn_tc.cu
 constexpr int kLinMaxBlocks = 148;       // one block per SM
 bool linattn_tc_dims(int dtype, int dk, int dv);
-LinPlan linattn_tc_plan(int B, int L, int Hk, int dv);
+LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens);
 cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s);
 
 }  // namespace hyena

@@ -743,25 +743,40 @@ HYENA_BOUNDS_READER(linattn_tc)
 
 bool linattn_tc_dims(int dtype, int dk, int dv) { return dtype == HYENA_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0; }
 
-// Segments: a chunk costs about 1, of the state pass 0.6 (no queries, no outputs); splitting adds two launches and
-// the passes over the segment states, about 4 chunks.
-LinPlan linattn_tc_plan(int B, int L, int Hk, int dv) {
-    LinPlan p{};
-    const int nv = dv <= 64 ? 64 : 128;
-    p.vtiles = (dv + nv - 1) / nv;
-    const double units = B > 0 ? (double)B * Hk * p.vtiles : 1.0;
-    const int chunks = L > 0 ? (L + kC - 1) / kC : 1;
-    auto waves = [](double x) { return (double)(long long)((x + kLinMaxBlocks - 1) / kLinMaxBlocks); };
-    double best = waves(units) * chunks;
-    int segc = chunks;
-    for (int want = 2; want <= chunks && want <= kLinMaxBlocks; ++want) {
-        const int sc = (chunks + want - 1) / want, ns = (chunks + sc - 1) / sc;
-        const double est = waves(units * ns) * sc + 0.6 * waves(units * (ns - 1)) * sc + 4.0;
-        if (est < best) { best = est; segc = sc; }
+// How a prompt is cut, by a model of the time in us (blocks take their items one after the other, so the longest one
+// counts).  A chunk of the main pass costs `base` + `query` for each query head of its key head, one of the state pass
+// `state`, the entry of an item (its state, the filling of the pipeline) `entry`; cutting adds the state pass, the
+// combination of the states and two launches.  Narrow tiles repeat the scores and the weighing of the keys, but give twice
+// the items: where sequences x heads leave SMs idle they cost less than a second pass over the tokens.
+// Measured for the model on whole grids: 128 x 128 tiles 5.0 us a chunk, 3.5 us without queries; 64 x 64 3.4 and 2.7.
+// Padded rows (lens) are taken to be half full.
+LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens) {
+    struct Cost { double base, query, state, entry; };
+    const double kCut = 15.0;
+    LinPlan best{};
+    double best_us = 0;
+    const int chunks = L > 0 ? (L + kC - 1) / kC : 1, Gq = H / Hk;
+    const double fill = lens ? 0.5 : 1.0;
+    auto waves = [&](double items) { const double w = (double)(long long)((items * fill + kLinMaxBlocks - 1) / kLinMaxBlocks); return w < 1 ? 1.0 : w; };
+    for (int nv = 64; nv <= (dv > 64 ? 128 : 64); nv += 64) {
+        const Cost c = dk <= 64 ? (nv == 64 ? Cost{0.4, 3.0, 2.7, 5.0} : Cost{0.5, 3.7, 3.0, 6.0})
+                                : (nv == 64 ? Cost{0.5, 3.5, 3.0, 6.0} : Cost{0.5, 4.5, 3.5, 10.0});
+        const int vtiles = (dv + nv - 1) / nv;
+        const double units = (double)(B > 0 ? B : 1) * Hk * vtiles;
+        for (int want = 1; want <= chunks && want <= kLinMaxBlocks; ++want) {
+            const int sc = (chunks + want - 1) / want, ns = (chunks + sc - 1) / sc;
+            double us = waves(units * ns) * (sc * (c.base + c.query * Gq) + c.entry);
+            if (ns > 1) us += waves(units * (ns - 1)) * (sc * c.state + c.entry / 2) + kCut;
+            if (best.vtiles == 0 || us < best_us) {
+                best_us = us;
+                best.vtiles = vtiles;
+                best.nv = nv;
+                best.seg_tokens = sc * kC;
+                best.nseg = ns;
+            }
+        }
     }
-    p.seg_tokens = segc * kC;
-    p.nseg = (chunks + segc - 1) / segc;
-    return p;
+    return best;
 }
 
 cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s) {
@@ -771,8 +786,8 @@ cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s
     if (!make_map(&m.q, a.q, a.B, a.L, a.H, a.dk, a.ldq) || !make_map(&m.k, a.k, a.B, a.L, a.Hk, a.dk, a.ldk) ||
         !make_map(&m.v, a.v, a.B, a.L, a.Hk, a.dv, a.ldv) || !make_map(&m.o, a.o, a.B, a.L, a.H, a.dv, (long long)a.H * a.dv))
         return cudaErrorInvalidValue;
-    if (a.dk <= 64) return a.dv <= 64 ? launch<64, 64>(m, a, (int)items, states_only, s) : launch<64, 128>(m, a, (int)items, states_only, s);
-    return a.dv <= 64 ? launch<128, 64>(m, a, (int)items, states_only, s) : launch<128, 128>(m, a, (int)items, states_only, s);
+    if (a.dk <= 64) return a.nv == 64 ? launch<64, 64>(m, a, (int)items, states_only, s) : launch<64, 128>(m, a, (int)items, states_only, s);
+    return a.nv == 64 ? launch<128, 64>(m, a, (int)items, states_only, s) : launch<128, 128>(m, a, (int)items, states_only, s);
 }
 
 }  // namespace hyena
