@@ -460,7 +460,7 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
 static int check_linattn(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
     if (dtype != HYENA_F32 && dtype != HYENA_BF16) return HYENA_ERR_ARG;
     if (B < 0 || L < 0 || H < 1 || Hk < 1 || H % Hk != 0 || dk < 1 || dv < 1) return HYENA_ERR_SHAPE;
-    if (dk > HYENA_MAX_HEAD_DIM || B > 65535) return HYENA_ERR_UNSUPPORTED;
+    if (dk > HYENA_MAX_HEAD_DIM || B > 65535 || L > HYENA_MAX_TOKENS) return HYENA_ERR_UNSUPPORTED;
     if ((long long)H * dv > 0x7fffffffll || (long long)H * dk > 0x7fffffffll) return HYENA_ERR_UNSUPPORTED;
     return HYENA_OK;
 }
@@ -557,6 +557,8 @@ int hyena_qk_norm_rotate(const void *q, const void *k, int dtype, int B, int L, 
     if (ldq < (long long)H * hd || ldqo < (long long)H * hd || ldk < (long long)Hk * hd || ldko < (long long)Hk * hd)
         return HYENA_ERR_SHAPE;
     if (B == 0 || L == 0 || H + Hk == 0) return HYENA_OK;
+    // positions are 32-bit
+    if (!positions && (long long)pos0 + L - 1 > 0x7fffffffll) return HYENA_ERR_ARG;
     if ((H > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out))) return HYENA_ERR_ARG;
     // in place needs the same rows: another stride would read what an earlier row has written
     if ((H > 0 && q == q_out && ldq != ldqo) || (Hk > 0 && k == k_out && ldk != ldko)) return HYENA_ERR_ARG;

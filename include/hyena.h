@@ -447,14 +447,15 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  *   workspace : device scratch, >= hyena_linattn_prefill_workspace_bytes() bytes,
  *               256-byte aligned; contents on entry are ignored.  Calls that may
  *               overlap need one each.
- * 1 <= dk <= HYENA_MAX_HEAD_DIM, 1 <= dv, H dv and Hk dv < 2^31; B <= 65535.
+ * 1 <= dk <= HYENA_MAX_HEAD_DIM, 1 <= dv, H dk and H dv < 2^31; B <= 65535,
+ * L <= HYENA_MAX_TOKENS.
  * Alignment: q, k, v, o to their element size, states 16 bytes (4 when dv is
  * not a multiple of 4), decay and lens 4.
  * Routes.  bf16 activations with dk <= 128, dk and dv multiples of 8, row
  * strides multiples of 8 elements and q, k, v, o 16-byte aligned run on the
  * tensor cores: chunks of 128 tokens, o from bf16 products with fp32
  * accumulation, the state in fp32 (its products take the weighted keys as sums
- * of three bf16 terms, exact to fp32).  Every other call runs in fp32 on the CUDA
+ * of four bf16 terms, which keep them to 2^-25).  Every other call runs in fp32 on the CUDA
  * cores.  hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the
  * error that hyena_linattn_prefill would return); host-only.
  * The tensor-core route waits on its own copies and products with bounded
@@ -467,6 +468,7 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * Empty problems (B == 0, or L == 0) are valid; L == 0 writes state_out.
  */
 #define HYENA_MAX_HEAD_DIM 256
+#define HYENA_MAX_TOKENS 0x7fffff00
 
 size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
 size_t hyena_linattn_prefill_error_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv);
@@ -503,7 +505,7 @@ typedef struct {
  *       for hyena_linattn_prefill; q_out, k_out the same shapes with rows ldqo,
  *       ldko apart.  q_out == q with ldqo == ldq (and the same for k) works in place.
  *       H == 0 or Hk == 0: only the other one (its pointers may be NULL).
- *   positions : [B][L] int32 device, or NULL: token t stands at pos0 + t.
+ *   positions : [B][L] int32 device, or NULL: token t stands at pos0 + t (below 2^31).
  *   prep is a HOST struct, read during the call.  hd even, <= HYENA_MAX_HEAD_DIM.
  */
 int hyena_qk_norm_rotate(const void *q, const void *k, int dtype, int B, int L, int H, int Hk, int hd,

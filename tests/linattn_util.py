@@ -6,8 +6,9 @@ output is off by at most K u M, where M is the same formula with every factor re
 value and K the number of roundings on the longest way from an input to the output:
  - a state entry: per token its product, its weight (formed from two table entries) and its sum; per
    block of 8 tokens a decay and an update, per segment one more of each (CUDA-core route);
-   so K <= 8 + 3 (8 + 2 L / 8).  On the tensor cores a chunk of 128 tokens is one sum of 3 * 128 terms
-   (three bf16 terms of each weighted key, which together keep it to 2^-24) and one decay: K <= 8 + 3 * 128
+   so K <= 8 + 3 (8 + 2 L / 8).  On the tensor cores a chunk of 128 tokens is one sum of the bf16 terms of
+   each weighted key (which together keep it to 2^-25) and one decay.  Three of a key's four terms can move a sum's
+   last place; the fourth, below 2^-16 of its product, adds under 128 * 2^-16 of one rounding: K <= 8 + 3 * 128
    + 2 L / 128, taken twice because the units add with truncation.
  - an output: the dk products with a state entry and their sum, besides.
 bf16 outputs add half a step, 2^-8 |o|.  On the tensor cores scores and states are rounded to bf16 as

@@ -52,3 +52,19 @@ def test_decode_and_norm_in_bounds(dtype, dk, dv):
         T.test_qk_norm_rotate(dk, dk, False, dtype)
         T.test_decode_with_norm_and_rotation(dtype, dk, dk // 4 * 2, False, 2, 2)
     _clean()
+
+
+@pytest.mark.parametrize("B,L,H,Hk,dk,dv", [(40, 150, 2, 2, 128, 128), (2, 2100, 8, 8, 128, 128), (38, 260, 4, 2, 64, 128),
+                                            (1, 1500, 4, 2, 128, 192)])
+def test_tiles_and_cuts_in_bounds(B, L, H, Hk, dk, dv):
+    T.test_prefill_tiles_and_cuts(B, L, H, Hk, dk, dv, True)
+    _clean()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", [0, 4, 1])
+@pytest.mark.parametrize("B,L,H,Hk,hd,rot", [(2, 700, 2, 1, 24, 8), (1, 3, 100, 1, 128, 128), (2, 601, 1, 3, 40, 20)])
+def test_norm_in_vectors_in_bounds(B, L, H, Hk, hd, rot, shift, dtype):
+    T.test_qk_vectors(B, L, H, Hk, hd, rot, shift, False, dtype)
+    T.test_qk_vectors(B, L, H, Hk, hd, rot, shift, True, dtype)
+    _clean()

@@ -32,7 +32,7 @@ def test_prefill_refusals(lib):
     for bad in (dict(B=-1), dict(L=-1), dict(H=0), dict(Hk=0), dict(H=3), dict(dk=0), dict(dv=0), dict(ldq=31), dict(ldk=15),
                 dict(ldv=15)):
         assert prefill(lib, **bad) == ERR_SHAPE, bad
-    for big in (dict(dk=257), dict(B=65536), dict(H=1 << 20, Hk=1 << 20, dv=1 << 12)):
+    for big in (dict(dk=257), dict(B=65536), dict(H=1 << 20, Hk=1 << 20, dv=1 << 12), dict(L=0x7fffff01)):
         assert prefill(lib, **big) == ERR_UNSUP, big
     for null in (dict(q=0), dict(state=0), dict(dec=0), dict(wsp=0)):
         assert prefill(lib, **null) == ERR_ARG, null
@@ -128,6 +128,17 @@ def test_qk_refusals(lib):
         assert qk(lib, prep=_prep(**kw)) == want, kw
     assert qk(lib, B=0) == OK and qk(lib, L=0) == OK
     assert qk(lib, H=0, Hk=0, q=0, k=0, qo=0, ko=0) == OK
+
+
+def test_qk_positions_stay_in_32_bits(lib):
+    f = lambda L, pos0, pos: lib.hyena_qk_norm_rotate(_p(FAKE), _p(FAKE), 1, 1, L, 1, 1, 8, 8, 8, _prep(), _p(pos), pos0,
+                                                      _p(2 * FAKE), _p(2 * FAKE), 8, 8, None)
+    assert f(2, 0x7fffffff, 0) == ERR_ARG and f(0x7fffffff, 2, 0) == ERR_ARG
+    assert lib.hyena_test_fail_next_launches(2) == OK          # the largest that fits passes the checks
+    try:
+        assert f(1, 0x7fffffff, 0) == ERR_CUDA and f(2, 0x7fffffff, FAKE) == ERR_CUDA
+    finally:
+        lib.hyena_test_fail_next_launches(0)
 
 
 def test_launch_failures_are_reported(lib):

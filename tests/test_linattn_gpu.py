@@ -99,6 +99,49 @@ def test_prefill_long_sequences_are_split(dtype, B, L, H, d):
     _run(B, L, H, H, d, d, dtype, lens=[L - 700 * i - 1 for i in range(B)])
 
 
+# Work that fills the GPU in 128-column tiles, whole and cut, with query heads that share a state; and 64-column tiles of
+# wide values where it does not.
+@pytest.mark.parametrize("B,L,H,Hk,dk,dv", [(40, 150, 2, 2, 128, 128), (2, 2100, 8, 8, 128, 128), (38, 260, 4, 2, 64, 128),
+                                            (40, 140, 6, 2, 104, 96), (1, 1500, 4, 2, 128, 192), (2, 300, 3, 1, 64, 128),
+                                            (150, 130, 1, 1, 32, 64)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_prefill_tiles_and_cuts(B, L, H, Hk, dk, dv, padded):
+    lens = [(L, 0, 1, L - 1, 129, L // 2)[b % 6] for b in range(B)] if padded else None
+    _run(B, L, H, Hk, dk, dv, BF16, lens=lens, carry=True, fused=True)
+
+
+@pytest.mark.parametrize("kind", [0.75, 0.7499, 0.76])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prefill_decays_around_the_scaling_rule(kind, dtype):
+    _run(2, 200, 4, 2, 64, 72, dtype, kind=kind, carry=True)
+
+
+@pytest.mark.parametrize("decay", [1.0, 0.76, 0.3])
+def test_prefill_large_values(decay):
+    """Scores up to 1e9 and outputs beyond 1e12 stay finite and within the bounds."""
+    q, k, v, _ = inputs(1, 140, 2, 2, 64, 64, BF16, 9)
+    q, k, v = _cuda(q * 1e4, k * 1e4, v * 1e3)
+    dec = decays(2, decay).cuda()
+    o, st = ops.linattn_prefill(q, k, v, dec, scale=0.125)
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(st).all())
+    check(o, st, reference(q, k, v, dec, 0.125), 140, 64, BF16, True)
+
+
+def test_prefill_chunks_follow_each_other():
+    """A prompt taken in pieces, each from the state of the one before, is the prompt taken whole (state: fp32 sums
+    in another grouping; outputs: the bounds of both)."""
+    q, k, v, S = _cuda(*inputs(2, 700, 4, 2, 64, 64, BF16, 31, carry=True))
+    dec = decays(2).cuda()
+    ref = reference(q, k, v, dec, 0.25, None, S)
+    outs, st, t = [], S.clone(), 0
+    for n in (1, 127, 128, 200, 244):
+        x = [y[:, t:t + n].contiguous() for y in (q, k, v)]
+        o, st = ops.linattn_prefill(*x, dec, scale=0.25, state_in=st, state=st)
+        outs.append(o)
+        t += n
+    check(torch.cat(outs, 1), st, ref, 700, 64, BF16, True)
+
+
 def test_prefill_lengths_outside_the_row_are_clamped():
     q, k, v, _ = _cuda(*inputs(2, 40, 2, 2, 32, 32, F32, 3))
     dec = decays(2).cuda()
@@ -179,6 +222,27 @@ def test_qk_norm_rotate(hd, rot, interleaved, dtype):
             for x, y, w in ((q, qo, wq), (k, ko, wk)):
                 want, tol = rotate_bound(x, w, 1e-6, f, p, interleaved, dtype)
                 assert bool(((y.double() - want).abs() <= tol).all()), float(((y.double() - want).abs() - tol).max())
+
+
+# Every vector width (8, 4, none) and group of lanes, many heads (several rounds of a block), several tokens to a block, and
+# bases and row strides that fit no vector.
+@pytest.mark.parametrize("B,L,H,Hk,hd,rot", [(1, 5, 3, 1, 80, 40), (2, 700, 2, 1, 24, 8), (1, 3, 2, 2, 12, 4), (1, 3, 100, 1, 128, 128),
+                                             (3, 500, 2, 2, 256, 8), (1, 1300, 7, 2, 64, 32), (2, 601, 1, 3, 40, 20),
+                                             (1, 2, 1, 70, 256, 256), (5, 333, 4, 4, 96, 0)])
+@pytest.mark.parametrize("shift", [0, 4, 1])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_qk_vectors(B, L, H, Hk, hd, rot, shift, interleaved, dtype):
+    g = torch.Generator().manual_seed(hd + rot + shift)
+    x = torch.randn((B, L, (H + Hk) * hd + 2 * shift), generator=g).to(dtype).cuda()
+    q = x[..., shift:shift + H * hd].unflatten(-1, (H, hd))
+    k = x[..., shift + H * hd:shift + (H + Hk) * hd].unflatten(-1, (Hk, hd))
+    wq, wk, f, prep = _prep(hd, rot, interleaved)
+    pos = torch.randint(0, 1 << 20, (B, L), generator=g, dtype=torch.int32).cuda()
+    qo, ko = ops.qk_norm_rotate(q, k, prep, positions=pos)
+    for a, y, w in ((q, qo, wq), (k, ko, wk)):
+        want, tol = rotate_bound(a, w, 1e-6, f, pos, interleaved, dtype)
+        assert bool(((y.double() - want).abs() <= tol).all()), float(((y.double() - want).abs() - tol).max())
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
