@@ -13,21 +13,28 @@
 //   P V     128 x dv x n     P as bf16 (tensor memory, over the scores) x V (shared), onto kColO
 //   state   dk x dv x n      weighted keys (tensor memory) x V (shared), from zero -> kColU
 // Roundings to bf16: the scores' P and the state's copy that multiplies q (operands only; both reach o, itself bf16).
-// The state itself stays fp32, in registers; its weighted keys enter as the sum of three bf16 terms, which is
-// exact: one term would leave 2^-9, two 2^-17 of each token in a state that every later token reads.  A chunk's
+// The state itself stays fp32, in registers; its weighted keys enter as the sum of four bf16 terms, which keeps them to
+// 2^-25: one term would leave 2^-9, two 2^-17 of each token in a state that every later token reads.  A chunk's
 // contribution is summed from zero and joined by one fp32 multiply-add: summing onto the state in tensor memory
-// cut off (the units truncate) 24 times a chunk at the state's size, 1e-6 and more over a long prompt.
+// cut off (the units truncate) at every product at the state's size, 1e-6 and more over a long prompt.
 //
-// Bound: 2 (dk + dv) (1 + 1) bytes per token and head of q, k, v, o against 2 C (dk + dv) + (2 + 6) dk dv operations:
-// memory-bound (at dk = dv = 128 the products need 55% of the time that the bytes need), if the chain
+// Bound: 2 (dk + dv) (1 + 1) bytes per token and head of q, k, v, o against 2 C (dk + dv) + (2 + 8) dk dv operations:
+// memory-bound (at dk = dv = 128 the products need 64% of the time that the bytes need), if the chain
 // scores -> P -> P V -> o of a chunk overlaps the loads of the next and the state's own chain.  Hence one
-// persistent block per SM (a chunk's tiles fill shared memory) with a role for each warp group:
+// persistent block per SM (a chunk's tiles fill shared memory) with a role for each warp or warp group:
 //   warp 0 loads K, V, Q; warp 1 stores O; warp 2 issues the products of the outputs, warp 3 those of the state
 //   warps 4-7   P group: a token row per thread: scores -> P, scaling of Q S, then O -> shared memory
-//   warps 8-11  K group: a row of the state (an entry of k) per thread: weighted keys -> tensor memory
-//   warps 12-15 S group: a row of the state per thread, in registers: its decay and sum, its bf16 copy
+//   warps 8-11  K group: keys -> weighted keys, by ldmatrix and packed bf16 fma -> tensor memory
+//   warps 12-19 S groups: half a row of the state per thread, in registers: its decay and sum, its bf16 copy
 // They meet at mbarriers only.  Every wait is bounded; on timeout the block records it in its error word,
 // drains its copies and products, frees tensor memory and returns.
+//
+// Measured (us, bf16): 64 sequences x 512 tokens x 16 heads of 128 x 128 141 (65% of measured HBM), 8 x 4096 x 8 heads 122
+// (34%), 65536 x 12 heads of 64 x 64 234 (26%: a second pass over K and V for the states).  What holds it there is
+// the length of a chunk's chains, not a unit: tensor cores 30% busy, issue slots 38%; a chunk takes 5.0 us where its
+// bytes take 3.0.  What was tried and not kept: the outputs by the S groups (their row of the state spills: 141 -> 160),
+// weighing keys by both P and K groups where there are no queries (no change), sleeping waits (no change), scores and
+// state rows loaded two pieces ahead (185: spills).
 //
 // Tensor-memory rows: tokens for the first three products, entries of k for the state.  With dk <= 64 the state's
 // rows 64..127 hold what the unused lanes give; nothing reads them.
