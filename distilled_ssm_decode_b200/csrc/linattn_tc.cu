@@ -295,7 +295,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         } else if (warp == 2) {
             // ------------------------------------------------------------ products of the outputs
             // the scores of the next query tile go out as soon as P V of this one has read P, while the outputs are stored
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 int cc = 0, qc = 0, sc = 0, id = blockIdx.x, c = 0, x = 0;
                 bool ok = true;
                 const uint32_t id_score = tc::idesc_bf16(128, 128, false), id_v = tc::idesc_bf16(128, NV, true);
@@ -329,7 +329,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     if ((x == 0 && !wait(G::KVFull + st, cc / G::kStages)) || !wait(G::QFull + qc % G::kQSlots, qc / G::kQSlots)) break;
                     tc::tc_fence_after();
                     const uint32_t q_lo = q_at(), k_lo = tc::sw128_desc_lo(sbase + st * G::kStage, 16);
-#pragma unroll 1
+#pragma unroll
                     for (int kb = 0; kb < G::kKB; ++kb)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
@@ -342,7 +342,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     if (!wait(G::OFree, qc + 1)) break;
                     tc::tc_fence_after();
                     if (has_state) {
-#pragma unroll 1
+#pragma unroll
                         for (int kb = 0; kb < G::kKB; ++kb)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
@@ -355,9 +355,9 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                     tc::tc_fence_after();
                     const uint32_t v_lo = tc::sw128_desc_lo(sbase + st * G::kStage + G::kKB * kBlk, kBlk);
                     const int steps = (min(kC, it.ntok - c * kC) + 15) / 16;
-#pragma unroll 1
-                    for (int ks = 0; ks < steps; ++ks)
-                        tc::mma_bf16_ta_sw128(tmem + kColO, tmem + kColP + 8 * ks, v_lo + ks * (2048 >> 4), id_v,
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks)
+                        if (ks < steps) tc::mma_bf16_ta_sw128(tmem + kColO, tmem + kColP + 8 * ks, v_lo + ks * (2048 >> 4), id_v,
                                               has_state || ks > 0);
                     tc::mma_commit(bar(G::T2Done));
                     ++qc;
@@ -379,7 +379,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         } else {
             // ------------------------------------------------------------ products of the state
             // the chunk's own contribution, from zero: kSub tokens of weighted keys at a time
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 int cc = 0, wc = 0;
                 bool ok = true;
                 const uint32_t id_v = tc::idesc_bf16(128, NV, true);

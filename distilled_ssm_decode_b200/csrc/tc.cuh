@@ -188,6 +188,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major)
            | ((uint32_t)(M >> 4) << 24);
 }
 
+// True for one lane of a converged warp.  Products issued under this test take their operands from uniform registers
+// (31 cycles each); under a test of the lane number every operand is moved there first (60 cycles, 100 in a rolled loop).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem], bf16 operands; issued by one thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
