@@ -67,8 +67,7 @@ static_assert(kColW + kWBufs * kWCols <= kTmemCols, "tensor memory");
 
 // Registers: the S groups hold half a row of the state in fp32.  The shares of the five warp groups must not exceed the
 // launch's 5 x 96 (checked before the first launch: a larger sum would wait for ever).
-constexpr int kRegsLaunch = 96, kRegsMisc = 56, kRegsS = 112;
-static_assert(kRegsMisc + 2 * kRegsLaunch + 2 * kRegsS <= 5 * kRegsLaunch, "register shares");
+constexpr int kRegsLaunch = 96;
 
 struct Maps {
     CUtensorMap q, k, v, o;
@@ -80,6 +79,8 @@ struct Geo {
     static constexpr int kStage = (kKB + kVB) * kBlk;                  // K, then V
     static constexpr int kQSlot = (kKB > kVB ? kKB : kVB) * kBlk;      // Q, then O
     static constexpr int kStages = NK + NV == 256 ? 2 : NK + NV == 192 ? 3 : 4, kQSlots = NK + NV == 128 ? 4 : 2;
+    static constexpr int kRegsMisc = NV == 128 ? 72 : 56, kRegsS = NV == 128 ? 104 : 112;
+    static_assert(kRegsMisc + 2 * kRegsLaunch + 2 * kRegsS <= 5 * kRegsLaunch, "register shares");
     static constexpr int kSBytes = NK * NV * 2;
     static constexpr int kSmQ = kStages * kStage;
     static constexpr int kSmS = kSmQ + kQSlots * kQSlot;
@@ -157,7 +158,9 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     if (tid == 0) {
         misc[0] = 0;
         misc[2] = 0;
-        for (int i = 0; i < G::kNumBars; ++i) tc::mbar_init(bar(i), G::count(i));
+        // without queries the K and the P group both weigh keys
+        for (int i = 0; i < G::kNumBars; ++i)
+            tc::mbar_init(bar(i), states_only && (i == G::KSync || (i >= G::VReady && i < G::T2Done)) ? 8 : G::count(i));
         tc::fence_mbar_init();
     } else if (tid == 32) {
         tc::prefetch_tensormap(&m.q);
@@ -173,7 +176,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[1];
-    auto uni = [&](bool x) -> bool { return __all_sync(0xffffffffu, x && !*abort); };
+    auto uni = [&](bool x) -> bool { return __all_sync(0xffffffffu, x); };
     // one arrival for each warp of a group (32 arrivals of a warp would be serialised)
     auto arrive = [&](int b) {
         __syncwarp();
@@ -218,7 +221,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kRegsMisc));
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             // K and V of the next chunk go out right behind the first queries of this one
@@ -312,8 +315,10 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 auto q_at = [&]() { return tc::sw128_desc_lo(sbase + G::kSmQ + (qc % G::kQSlots) * G::kQSlot, 16); };
                 bool live = settle();
                 if (states_only) {
-                    for (; live && ok; ++cc) {           // the state's warp gives the stages back; this is its second arrival
-                        if (!wait(G::KVFull + cc % G::kStages, cc / G::kStages)) break;
+                    // the stage's second arrival (the first is the state's warp's), once both groups that weigh keys have
+                    // passed it: one of them may have no piece of this chunk
+                    for (; live && ok; ++cc) {
+                        if (!wait(G::VReady + cc % G::kStages, cc / G::kStages)) break;
                         tc::mma_commit(bar(G::KVEmpty + cc % G::kStages));
                         if (++c == it.nck) {
                             c = 0;
@@ -414,13 +419,13 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 tc::mbar_wait(bar(G::DrainU), 0, never);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 8 && !states_only) {
         // ------------------------------------------------------------ P group
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int qc = 0, hk_cur = -1, met = 0;
         float f_row = 0.f;          // scale g^(i+1) of this row
-        bool up = false, ok = !states_only;
+        bool up = false, ok = true;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
             // the head's powers (this group writes its own table for itself)
@@ -489,10 +494,11 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 }
             }
         }
-        if (!ok && !states_only) *abort = 1;
+        if (!ok) *abort = 1;
     } else if (warp < 12) {
         // ------------------------------------------------------------ K group
-        const int w = warp & 3, d = 32 * w + lane;
+        // without queries the P group weighs every other piece of keys
+        const int w = warp & 3, d = 32 * w + lane, kg = warp < 8 ? 1 : 0;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int cc = 0, wc = 0, hk_cur = -1, n_cur = 0, met = 0;         // the table's head and chunk length
         bool ok = true;
@@ -502,7 +508,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 const int st = cc % G::kStages, n = min(kC, it.ntok - c * kC);
                 if (it.hk != hk_cur || n != n_cur) {
                     if (!(ok = meet(G::KSync, met))) break;
-                    if (d < kC / 2) {
+                    if (d < kC / 2 && kg == 0) {
                         const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
                         rw[d] = split_weights((float)decay_pow(g, max(n - 1 - 2 * d, 0)), (float)decay_pow(g, max(n - 2 - 2 * d, 0)));
                     }
@@ -525,8 +531,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 arrive(G::VReady + st);
                 for (int h = 0; h * kSub < n; ++h, ++wc) {
                     const int wb = wc % kWBufs;
-                    if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
-                    tc::tc_fence_after();
+                    if (states_only && wb != kg) continue;
                     // x = w k as four bf16 terms.  The product of two bf16 numbers is the sum of its rounding and
                     // of what fma leaves, both exact: k w1 = t0 + e0, k w2 = t1 + e1; the last, k w3 + e1, is
                     // rounded at 2^-26 |x|.  Two tokens to a column, the terms kSub / 2 columns apart.
@@ -535,12 +540,18 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
 #pragma unroll
                         for (int m = 0; m < 4; ++m) pwt[m] = rw[h * (kSub / 2) + 4 * m + (lane & 3)];
                         const uint32_t k_row = kt + (w / 2) * kBlk + (h * kSub + (lane >> 4) * 8 + (lane & 7)) * 128;
-#pragma unroll 1
+                        uint32_t xs[2][8];
+#pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {              // 16 entries of k
                             const int ch = (w & 1) * 4 + hf * 2 + ((lane >> 3) & 1);      // this lane's 16-byte piece of its row
-                            uint32_t x[8];
-                            tc::ldmatrix_x4_trans(k_row + ((ch ^ (lane & 7)) << 4), x);
-                            tc::ldmatrix_x4_trans(k_row + 16 * 128 + ((ch ^ (lane & 7)) << 4), x + 4);
+                            tc::ldmatrix_x4_trans(k_row + ((ch ^ (lane & 7)) << 4), xs[hf]);
+                            tc::ldmatrix_x4_trans(k_row + 16 * 128 + ((ch ^ (lane & 7)) << 4), xs[hf] + 4);
+                        }
+                        if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t *x = xs[hf];
                             if (n != kC) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
@@ -566,7 +577,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                             for (int y = 0; y < kTerms; ++y) tc::tmem_st_16x128b_x4(cols + y * (kSub / 2), t[y]);
                         }
                         tc::tmem_wait_st();
-                    }
+                    } else if (!(ok = uni(tc::mbar_wait(bar(G::WFree + wb), ((wc / kWBufs) & 1) ^ 1, abort)))) break;
                     tc::tc_fence_before();
                     arrive(G::WReady + wb);
                 }
@@ -576,7 +587,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     } else {
         // ------------------------------------------------------------ S groups
         // each has half of the columns of the state's rows, in registers
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kRegsS));
         constexpr int NH = G::kNH;
         const int w = warp & 3, d = 32 * w + lane, sg = (warp - 12) >> 2;        // d: row of the state
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);

@@ -110,6 +110,15 @@ def test_prefill_tiles_and_cuts(B, L, H, Hk, dk, dv, padded):
     _run(B, L, H, Hk, dk, dv, BF16, lens=lens, carry=True, fused=True)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_prefill_cut_prompt_with_short_rows(dk, dv):
+    """A long padded prompt, cut, whose rows are mostly a few tokens: chunks of one piece of keys follow each other."""
+    n = 48
+    lens = [2049] + [(i * 7) % 37 for i in range(n - 1)]
+    _run(n, 2049, 2, 2, dk, dv, BF16, lens=lens, carry=True)
+    _run(2, 2049, 1, 1, dk, dv, BF16, lens=[2049, 3])
+
+
 @pytest.mark.parametrize("kind", [0.75, 0.7499, 0.76])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_prefill_decays_around_the_scaling_rule(kind, dtype):
