@@ -493,7 +493,7 @@ int hyena_linattn_prefill_uses_tensor_cores(int dtype, int B, int L, int H, int 
     int st = check_linattn(dtype, B, L, H, Hk, dk, dv);
     if (st == HYENA_OK) st = check_strides(H, Hk, dk, dv, ldq, ldk, ldv);
     if (st != HYENA_OK) return st;
-    return linattn_uses_tc(dtype, dk, dv, ldq, ldk, ldv, q, k, v, o) ? 1 : 0;
+    return linattn_uses_tc(dtype, L, H, Hk, dk, dv, ldq, ldk, ldv, q, k, v, o) ? 1 : 0;
 }
 
 int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk, int dk,

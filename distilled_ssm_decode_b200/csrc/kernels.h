@@ -105,7 +105,7 @@ cudaError_t launch_modal_truncate(const float2 *lam, const float2 *R, int H, int
 // linattn.cu, linattn_tc.cu (linear attention with a decay for each head, over a prompt)
 size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
 size_t linattn_err_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv);
-bool linattn_uses_tc(int dtype, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
+bool linattn_uses_tc(int dtype, int L, int H, int Hk, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
                      const void *k, const void *v, const void *o);
 cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, int dtype, int B, int L, int H, int Hk,
                                    int dk, int dv, long long ldq, long long ldk, long long ldv, const float *decay,

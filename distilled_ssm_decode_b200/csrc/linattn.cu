@@ -272,9 +272,13 @@ cudaError_t launch_simt(const LinArgs &a, bool states_only, cudaStream_t s) {
 
 HYENA_BOUNDS_READER(linattn)
 
-bool linattn_uses_tc(int dtype, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
+bool linattn_uses_tc(int dtype, int L, int H, int Hk, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,
                      const void *k, const void *v, const void *o) {
     auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    // A prompt of one block of tokens (kT) costs the CUDA cores less than the tensor cores' pipeline takes to fill:
+    // 64 x 16 states of 128 x 128, carried, 8 tokens 52 us against 100, 16 tokens 85 against 101; 31 x 12 of 64 x 128 with 3
+    // query heads each, 8 tokens 23 against 31 (16: 40); 200 x 8 of 128 x 128 with 4, 8 tokens 184 against 117.
+    if (L <= kT && (long long)L * (H / Hk) <= 3 * kT) return false;
     return linattn_tc_dims(dtype, dk, dv) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0 && ok(q) && ok(k) && ok(v) && ok(o);
 }
 
@@ -295,7 +299,7 @@ cudaError_t launch_linattn_prefill(const void *q, const void *k, const void *v, 
                                    int dk, int dv, long long ldq, long long ldk, long long ldv, const float *decay,
                                    float scale, const int *lens, const float *state_in, void *o, float *state_out,
                                    void *ws, cudaStream_t s) {
-    const bool tc = linattn_uses_tc(dtype, dk, dv, ldq, ldk, ldv, q, k, v, o);
+    const bool tc = linattn_uses_tc(dtype, L, H, Hk, dk, dv, ldq, ldk, ldv, q, k, v, o);
     const LinPlan p = tc ? linattn_tc_plan(B, L, H, Hk, dk, dv, lens != nullptr) : simt_plan(B, L, Hk, dv);
     LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.o = o;

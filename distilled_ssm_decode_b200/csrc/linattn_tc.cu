@@ -642,6 +642,13 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 }
                 if (NV == 64 && !(ok = meet(G::SSync, met))) break;
             }
+            // the next item's entering state on its way to L2: read cold it would cost a dependent trip to memory
+            if (init && id + (int)gridDim.x < items) {
+                const Item nx = item_of(a, id + gridDim.x, NV);
+                const long long base = (long long)nx.seg * a.init_stride + ((long long)nx.b * a.Hk + nx.hk) * a.dk * a.dv;
+                for (int i = sg * 128 + d; i < (a.dk * a.dv + 31) / 32; i += 256)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.init + base + 32ll * i));
+            }
             // c = -1: only the copy of the entering state
             for (int c = -1; c < it.nck; ++c) {
                 if (c >= 0) {

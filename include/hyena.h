@@ -451,13 +451,14 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * L <= HYENA_MAX_TOKENS.
  * Alignment: q, k, v, o to their element size, states 16 bytes (4 when dv is
  * not a multiple of 4), decay and lens 4.
- * Routes.  bf16 activations with dk <= 128, dk and dv multiples of 8, row
- * strides multiples of 8 elements and q, k, v, o 16-byte aligned run on the
- * tensor cores: chunks of 128 tokens, o from bf16 products with fp32
- * accumulation, the state in fp32 (its products take the weighted keys as sums
- * of four bf16 terms, which keep them to 2^-25).  Every other call runs in fp32 on the CUDA
- * cores.  hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the
- * error that hyena_linattn_prefill would return); host-only.
+ * Routes.  bf16 activations with dk <= 128, dk and dv multiples of 8, more than 8
+ * tokens (or more than 24 query vectors for a state: L H / Hk), row strides
+ * multiples of 8 elements and q, k, v, o 16-byte aligned run on the tensor cores:
+ * chunks of 128 tokens, o from bf16 products with fp32 accumulation, the state in
+ * fp32 (its products take the weighted keys as sums of four bf16 terms, which keep
+ * them to 2^-25).  Every other call runs in fp32 on the CUDA cores.
+ * hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the error that
+ * hyena_linattn_prefill would return); host-only.
  * The tensor-core route waits on its own copies and products with bounded
  * waits: the int32s from byte hyena_linattn_prefill_error_offset() to the end of
  * the queried workspace are all 0 after a successful run of that route; another

@@ -48,7 +48,7 @@ def _run(B, L, H, Hk, dk, dv, dtype, *, lens=None, carry=False, fused=False, kin
     ws = torch.full((ops.linattn_prefill_workspace_bytes(*dims),), 255, dtype=torch.uint8, device="cuda")
     o, st = ops.linattn_prefill(qd, kd, vd, dec, scale=scale, lens=ln, state_in=Sd, o=o, workspace=ws)
     tc = ops.linattn_prefill_uses_tensor_cores(qd, kd, vd, o)
-    assert tc == (dtype == BF16 and dk <= 128 and dk % 8 == 0 and dv % 8 == 0)
+    assert tc == (dtype == BF16 and dk <= 128 and dk % 8 == 0 and dv % 8 == 0 and (L > 8 or L * H // Hk > 24))
     if tc:
         assert ops.linattn_error(ws, *dims) == 0, "a wait gave up"
     ref = reference(qd, kd, vd, dec, scale, ln, Sd)
@@ -108,6 +108,12 @@ def test_prefill_long_sequences_are_split(dtype, B, L, H, d):
 def test_prefill_tiles_and_cuts(B, L, H, Hk, dk, dv, padded):
     lens = [(L, 0, 1, L - 1, 129, L // 2)[b % 6] for b in range(B)] if padded else None
     _run(B, L, H, Hk, dk, dv, BF16, lens=lens, carry=True, fused=True)
+
+
+@pytest.mark.parametrize("L,H,Hk", [(1, 25, 1), (5, 10, 2), (8, 16, 4), (8, 3, 1), (8, 4, 1), (9, 1, 1), (1, 2, 2)])
+def test_prefill_short_prompts_on_either_route(L, H, Hk):
+    _run(3, L, H, Hk, 64, 128, BF16, carry=True)
+    _run(200, L, H, Hk, 128, 128, BF16, lens=[b % (L + 1) for b in range(200)], carry=True)
 
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
