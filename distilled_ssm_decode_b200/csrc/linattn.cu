@@ -22,7 +22,7 @@ constexpr int kT = 8;            // tokens of a block
 constexpr int kTV = 64;          // state columns of a thread block
 
 template <class Act, int RK>
-__global__ void __launch_bounds__(kThreads, RK <= 16 ? 2 : 1) linattn_kernel(const LinArgs a, int states_only) {
+__global__ void __launch_bounds__(kThreads, 2) linattn_kernel(const LinArgs a, int states_only) {
     using T = typename Act::T;
     constexpr int DKP = kWarps * RK;             // dk, padded with zeros
     constexpr int LD = DKP + 16;                 // row stride: rows of the score products fall into different banks

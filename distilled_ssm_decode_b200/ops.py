@@ -110,11 +110,13 @@ def using_library(path: str):
     with _lock:
         prev = _lib
         _lib = other
+    linattn_prefill_workspace_bytes.cache_clear()        # the looked-up sizes are another build's
     try:
         yield other
     finally:
         with _lock:
             _lib = prev
+        linattn_prefill_workspace_bytes.cache_clear()
 
 
 def bounds_check():
