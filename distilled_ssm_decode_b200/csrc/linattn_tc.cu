@@ -29,12 +29,12 @@
 // They meet at mbarriers only.  Every wait is bounded; on timeout the block records it in its error word,
 // drains its copies and products, frees tensor memory and returns.
 //
-// Measured (us, bf16): 64 sequences x 512 tokens x 16 heads of 128 x 128 141 (65% of measured HBM), 8 x 4096 x 8 heads 122
-// (34%), 65536 x 12 heads of 64 x 64 234 (26%: a second pass over K and V for the states).  What holds it there is
-// the length of a chunk's chains, not a unit: tensor cores 30% busy, issue slots 38%; a chunk takes 5.0 us where its
-// bytes take 3.0.  What was tried and not kept: the outputs by the S groups (their row of the state spills: 141 -> 160),
-// weighing keys by both P and K groups where there are no queries (no change), sleeping waits (no change), scores and
-// state rows loaded two pieces ahead (185: spills).
+// Measured (us of the launches alone, bf16): 64 sequences x 512 tokens x 16 heads of 128 x 128 138 (67% of measured HBM),
+// 8 x 4096 x 8 heads 93 (45%), 65536 x 12 heads of 64 x 64 195 (32%: a second pass over K and V for the states).  What holds
+// it there is the length of a chunk's chains, not a unit: tensor cores 42% busy, issue slots 45%; a chunk takes 5.0 us where
+// its bytes take 3.0.  What was tried and not kept: the outputs by the S groups (their row of the state spills: 141 ->
+// 160), sleeping waits (no change), scores and state rows loaded two pieces ahead (185: spills), the next head's
+// powers computed ahead (142).
 //
 // Tensor-memory rows: tokens for the first three products, entries of k for the state.  With dk <= 64 the state's
 // rows 64..127 hold what the unused lanes give; nothing reads them.
@@ -773,7 +773,8 @@ bool linattn_tc_dims(int dtype, int dk, int dv) { return dtype == HYENA_BF16 && 
 // `state`, the entry of an item (its state, the filling of the pipeline) `entry`; cutting adds the state pass, the
 // combination of the states and two launches.  Narrow tiles repeat the scores and the weighing of the keys, but give twice
 // the items: where sequences x heads leave SMs idle they cost less than a second pass over the tokens.
-// Measured for the model on whole grids: 128 x 128 tiles 5.0 us a chunk, 3.5 us without queries; 64 x 64 3.4 and 2.7.
+// The figures were measured on whole grids when the rule was made; since then the passes have become faster by a tenth
+// (128 x 128 5.0 us a chunk, 128 x 64 2.9, 64 x 64 3.0 and 1.9 without queries), in proportion enough to leave the choices.
 // Padded rows (lens) are taken to be half full.
 LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens) {
     struct Cost { double base, query, state, entry; };
