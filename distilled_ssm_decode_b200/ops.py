@@ -485,24 +485,30 @@ def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
     projection's output has them."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     sh, st = t.shape, t.stride()
     if len(sh) != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    rows, heads, width = sh[0], sh[-2], sh[-1]
-    n = heads * width
-    if 0 in sh:
-        return n
-    if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if dim == 3 or sh[1] == 1:
-        ld = st[0] if rows > 1 else n
+    if dim == 3:
+        rows, heads, width = sh
+        s_row, s_head, s_entry = st
+        tokens, s_token = 1, 0
     else:
-        ld = st[1]
-        if rows > 1 and st[0] != sh[1] * ld:
+        rows, tokens, heads, width = sh
+        s_row, s_token, s_head, s_entry = st
+    n = heads * width
+    if n == 0 or rows == 0 or tokens == 0:
+        return n
+    if (s_entry != 1 and width > 1) or (s_head != width and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if tokens == 1:
+        ld = s_row if rows > 1 else n
+    else:
+        ld = s_token
+        if rows > 1 and s_row != tokens * ld:
             raise ValueError(f"{name}: batch rows must follow each other at the token stride")
     if ld < n:
         raise ValueError(f"{name}: tokens overlap")
@@ -513,6 +519,8 @@ def _plain(t, name: str, dtype, shape, device):
     """The address of a contiguous tensor of this dtype, shape and device (None: None)."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     _cuda(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
