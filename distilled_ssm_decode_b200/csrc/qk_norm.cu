@@ -4,7 +4,8 @@
 // It first issues the loads of its heads (VEC entries per lane, PP lanes per head), then tabulates the
 // tokens' cos and sin in shared memory -- they are the same for all heads, so the fp64 angles cost one evaluation
 // per (token, pair), not per entry, and run while the loads are in flight -- and then norms, rotates and stores.
-// The other entry of a pair comes from the lane that has it, by a shuffle.  Sizes, strides or pointers that do not
+// With whole heads rotated a lane has both entries of its pairs (56 us where shuffles took 68, 8 x 4096 tokens of 2 x 8
+// heads of 128); otherwise the other entry comes from the lane that has it, by a shuffle.  Sizes, strides or pointers that do not
 // fit a vector take the scalar kernel (a warp per head).
 #include "kernels.h"
 #include "qk_norm.cuh"
@@ -125,6 +126,21 @@ template <class Act, int VEC> struct Raw {
             *static_cast<uint32_t *>(p) = r[0];
         }
     }
+    // the two halves from two places
+    __device__ __forceinline__ void load(const void *p, const void *q) {
+        Raw<Act, VEC / 2> a, b;
+        a.load(p);
+        b.load(q);
+#pragma unroll
+        for (int i = 0; i < kWords / 2; ++i) { r[i] = a.r[i]; r[kWords / 2 + i] = b.r[i]; }
+    }
+    __device__ __forceinline__ void store(void *p, void *q) const {
+        Raw<Act, VEC / 2> a, b;
+#pragma unroll
+        for (int i = 0; i < kWords / 2; ++i) { a.r[i] = r[i]; b.r[i] = r[kWords / 2 + i]; }
+        a.store(p);
+        b.store(q);
+    }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (Act::bytes == 4) return __uint_as_float(r[i]);
         else return __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
@@ -145,18 +161,20 @@ template <class Act, int VEC> struct Raw {
 // r (x A + y B) with y the pair's other entry and A = w cos, B = -+ w_y sin fixed for the group's token (A = w, B = 0
 // without rotation), so a head costs three operations per entry beside its norm.
 // Pairs (i, i + rot/2) need rot/2 to be a multiple of VEC, so that a lane's entries lie on one side.
-enum { kNoRotation, kHalves, kNeighbours };
+// kWhole: pairs (i, i + hd/2) of whole heads, both entries of a pair in one lane; kHalves: (i, i + rot/2) of a part
+enum { kNoRotation, kHalves, kNeighbours, kWhole };
 template <class Act, int VEC, int PP, int MODE>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a) {
     using T = typename Act::T;
     using R = Raw<Act, VEC>;
-    constexpr int kGroups = kThreads / PP, U = R::kWords > 4 ? 2 : 4, VL = VEC < 4 ? VEC : 4;
+    constexpr int kGroups = kThreads / PP, U = R::kWords > 4 ? 2 : 4, HV = VEC / 2;
     __shared__ __align__(16) float cs[2][kMaxTile * kMaxHalf];      // cos, sin
     __shared__ __align__(16) float ws[2][HYENA_MAX_HEAD_DIM];       // norm weights of q and k
     const int tid = threadIdx.x, l = tid % PP, grp = tid / PP, half = a.p.rot >> 1;
     const int gpt = kGroups / a.tile, tt = grp / gpt, slot = grp % gpt;
-    const int e = l * VEC, side = MODE != kHalves || e >= 2 * half ? 0 : e < half ? 1 : -1;
-    const bool on = e < a.hd;
+    const int e = MODE == kWhole ? l * HV : l * VEC, far = MODE == kWhole ? a.hd / 2 - HV : 0;      // far: from its first half's end to its second half
+    const int side = MODE != kHalves || e >= 2 * half ? 0 : e < half ? 1 : -1;
+    const bool on = l * VEC < a.hd;
     const int mate = (tid & 31) + side * (half / VEC);              // the lane with the pairs' other entries
     const long long t = (long long)blockIdx.x * a.tile + tt;
     const int nt = (int)min((long long)a.tile, a.ntok - (long long)blockIdx.x * a.tile);
@@ -172,18 +190,22 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
 #pragma unroll
             for (int i = 0; i < R::kWords; ++i) x[s][u].r[i] = 0u;
             const long long xat = at + (long long)u * gpt * a.hd;
-            if (on && tt < nt && base + u * gpt + slot < heads && HB_OK(xat + VEC - 1, ext)) x[s][u].load(src + xat);
+            if (on && tt < nt && base + u * gpt + slot < heads && HB_OK(xat + far + VEC - 1, ext)) {
+                if constexpr (MODE == kWhole) x[s][u].load(src + xat, src + xat + a.hd / 2);
+                else x[s][u].load(src + xat);
+            }
         }
     };
+    constexpr int kRead = MODE == kWhole ? HV : VEC;
     auto read = [&](const float *p, float *v) {
+        if constexpr (kRead == 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(p);
+            v[0] = f.x; v[1] = f.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; i += VL) {
-            if constexpr (VL == 4) {
+            for (int i = 0; i < kRead; i += 4) {
                 const float4 f = *reinterpret_cast<const float4 *>(p + i);
                 v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-            } else {
-                const float2 f = *reinterpret_cast<const float2 *>(p + i);
-                v[i] = f.x; v[i + 1] = f.y;
             }
         }
     };
@@ -191,7 +213,12 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
     auto angles = [&]() {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) { c[i] = 1.f; sn[i] = 0.f; }
-        if (MODE == kHalves && side) {
+        if (MODE == kWhole) {
+            if (on) {
+                read(cs[0] + tt * half + e, c);
+                read(cs[1] + tt * half + e, sn);
+            }
+        } else if (MODE == kHalves && side) {
             const int at = tt * half + (side > 0 ? e : e - half);
             read(cs[0] + at, c);
             read(cs[1] + at, sn);
@@ -219,16 +246,27 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
         {
             float w0[VEC], w1[VEC];
             read(ws[s] + (on ? e : 0), w0);
-            if (MODE != kHalves) {
+            if constexpr (MODE == kWhole) {
+                read(ws[s] + (on ? e + a.hd / 2 : 0), w1);
+#pragma unroll
+                for (int i = 0; i < HV; ++i) {
+                    A[i] = w0[i] * c[i];
+                    B[i] = -w1[i] * sn[i];
+                    A[HV + i] = w1[i] * c[i];
+                    B[HV + i] = w0[i] * sn[i];
+                }
+            } else if (MODE != kHalves) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) w1[i] = w0[i ^ 1];
             } else {
                 read(ws[s] + (on ? e + side * half : 0), w1);
             }
+            if constexpr (MODE != kWhole) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                A[i] = w0[i] * c[i];
-                B[i] = w1[i] * sn[i];
+                for (int i = 0; i < VEC; ++i) {
+                    A[i] = w0[i] * c[i];
+                    B[i] = w1[i] * sn[i];
+                }
             }
         }
 #pragma unroll
@@ -255,7 +293,10 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
                 float y0 = 0.f, y1 = 0.f;
-                if (MODE == kHalves) {
+                if (MODE == kWhole) {
+                    y0 = z.get((i + HV) % VEC);
+                    y1 = z.get((i + 1 + HV) % VEC);
+                } else if (MODE == kHalves) {
                     y0 = y.get(i);
                     y1 = y.get(i + 1);
                 } else if (MODE == kNeighbours && e + i < 2 * half) {
@@ -265,18 +306,25 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
                 o.set2(i, r * fmaf(z.get(i), A[i], y0 * B[i]), r * fmaf(z.get(i + 1), A[i + 1], y1 * B[i + 1]));
             }
             const long long xat = at + (long long)u * gpt * a.hd;
-            if (on && tt < nt && base + u * gpt + slot < heads && HB_OK(xat + VEC - 1, ext)) o.store(dst + xat);
+            if (on && tt < nt && base + u * gpt + slot < heads && HB_OK(xat + far + VEC - 1, ext)) {
+                if constexpr (MODE == kWhole) o.store(dst + xat, dst + xat + a.hd / 2);
+                else o.store(dst + xat);
+            }
         }
     };
     load(0, 0);
     load(1, 0);
     const long long tb = (long long)blockIdx.x * a.tile;
-    for (int i = tid; i < nt * half; i += kThreads) {
-        const long long ta = tb + i / half;
+    // a warp per token, or all warps for a single one
+    const bool one = nt == 1;
+    for (int i = one ? 0 : tid >> 5; i < nt; i += kThreads / 32) {
+        const long long ta = tb + i;
         const int pos = a.pos ? a.pos[HB_IDX(ta, a.ntok)] : a.pos0 + (int)(ta % a.L);
-        const float2 v = rotation_of(pos, a.p.inv_freq[HB_IDX(i % half, half)]);
-        cs[0][i] = v.x;
-        cs[1][i] = v.y;
+        for (int p = one ? tid : tid & 31; p < half; p += one ? kThreads : 32) {
+            const float2 v = rotation_of(pos, a.p.inv_freq[HB_IDX(p, half)]);
+            cs[0][i * half + p] = v.x;
+            cs[1][i * half + p] = v.y;
+        }
     }
     for (int i = tid; i < 2 * a.hd; i += kThreads) {
         const int s = i >= a.hd, j = i - s * a.hd;
@@ -298,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_vec_kernel(const QKArgs a
 template <class Act, int VEC, int PP>
 void launch_mode(const QKArgs &a, unsigned blocks, cudaStream_t s) {
     if (a.p.rot == 0) qk_norm_vec_kernel<Act, VEC, PP, kNoRotation><<<blocks, kThreads, 0, s>>>(a);
+    else if (!a.p.interleaved && a.p.rot == a.hd) qk_norm_vec_kernel<Act, VEC, PP, kWhole><<<blocks, kThreads, 0, s>>>(a);
     else if (!a.p.interleaved) qk_norm_vec_kernel<Act, VEC, PP, kHalves><<<blocks, kThreads, 0, s>>>(a);
     else qk_norm_vec_kernel<Act, VEC, PP, kNeighbours><<<blocks, kThreads, 0, s>>>(a);
 }
@@ -329,13 +378,13 @@ cudaError_t launch_qk_norm(const void *q, const void *k, int dtype, int B, int L
     a.p = QKPrepArgs{p.norm, p.eps, p.q_weight, p.k_weight, p.rot_dim, p.inv_freq, p.interleaved};
     // Vectors of 8 or 4 entries: the widest that divides the head, the strides and (pairs (i, i + rot/2)) rot / 2,
     // with the pointers aligned to it and the head within a warp.  Measured, bf16, 8 x 4096 tokens
-    // of 2 x 8 heads of 128: 68 us (3.9 TB/s of 6.5 measured; 155 us with the scalar kernel alone), fp32, 3 x 1999
-    // tokens of 8 heads of 80: 12.8 us (20 us).
+    // of 2 x 8 heads of 128: 56 us (4.8 TB/s of 6.5 measured; 155 us with the scalar kernel alone), fp32, 3 x 1999
+    // tokens of 8 heads of 80: 13 us (20 us).
     const int bytes = dtype == HYENA_BF16 ? 2 : 4;
     int vec = 8;
     auto fits = [&](int n) {
         auto at = [&](const void *x) { return reinterpret_cast<uintptr_t>(x) % ((size_t)min(16, n * bytes)) == 0; };
-        return hd % n == 0 && hd / n <= 32 && (p.interleaved || (p.rot_dim / 2) % n == 0) && ldq % n == 0 && ldk % n == 0 &&
+        return hd % n == 0 && hd / n <= 32 && (p.interleaved || p.rot_dim == hd || (p.rot_dim / 2) % n == 0) && ldq % n == 0 && ldk % n == 0 &&
                ldqo % n == 0 && ldko % n == 0 && at(q) && at(k) && at(qo) && at(ko);
     };
     while (vec > 2 && !fits(vec)) vec /= 2;
