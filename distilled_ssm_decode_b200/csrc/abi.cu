@@ -477,6 +477,12 @@ static int check_prep(const hyena_qk_prep *p, int hd) {
     return HYENA_OK;
 }
 
+int hyena_test_linattn_hold(int enable) {
+    if (enable != 0 && enable != 1) return HYENA_ERR_ARG;
+    linattn_hold(enable);
+    return HYENA_OK;
+}
+
 size_t hyena_linattn_prefill_workspace_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv) {
     if (check_linattn(dtype, B, L, H, Hk, dk, dv) != HYENA_OK) return 0;
     return linattn_ws_bytes(dtype, B, L, H, Hk, dk, dv);

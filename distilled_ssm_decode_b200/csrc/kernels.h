@@ -103,6 +103,7 @@ cudaError_t launch_modal_truncate(const float2 *lam, const float2 *R, int H, int
                                   float2 *lam_out, float2 *R_out, double *bound, double *err_l2, cudaStream_t s);
 
 // linattn.cu, linattn_tc.cu (linear attention with a decay for each head, over a prompt)
+void linattn_hold(int enable);           // test hook
 size_t linattn_ws_bytes(int dtype, int B, int L, int H, int Hk, int dk, int dv);
 size_t linattn_err_offset(int dtype, int B, int L, int H, int Hk, int dk, int dv);
 bool linattn_uses_tc(int dtype, int L, int H, int Hk, int dk, int dv, long long ldq, long long ldk, long long ldv, const void *q,

@@ -33,6 +33,7 @@ struct LinArgs {
     int vtiles, nv;          // column tiles of a state, their width
     int *err;                // tensor-core route: an error word for each block
     int nerr;
+    int hold;                // tests: block 0 never signals its state products, so that a wait runs out
 };
 
 // tokens of row b
@@ -52,6 +53,6 @@ struct LinPlan {
 constexpr int kLinMaxBlocks = 148;       // one block per SM
 bool linattn_tc_dims(int dtype, int dk, int dv);
 LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens);
-cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s);
+cudaError_t launch_linattn_tc(LinArgs a, bool states_only, cudaStream_t s);
 
 }  // namespace hyena

@@ -263,13 +263,14 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         if (states_only) load_kv();
                     }
                 }
-                if (!ok) {
-                    *abort = 1;
-                    for (int j = max(0, cc - G::kStages); j < cc; ++j)
-                        tc::mbar_wait(bar(G::KVFull + j % G::kStages), (j / G::kStages) & 1, never);
-                    for (int j = max(0, qc - G::kQSlots); j < qc; ++j)
-                        tc::mbar_wait(bar(G::QFull + j % G::kQSlots), (j / G::kQSlots) & 1, never);
-                }
+                if (!ok) *abort = 1;
+                // No copy may be in flight when the block leaves: another role's wait can run out after this one has issued
+                // its last copies, so they are waited for here either way (without a timeout each has a consumer that
+                // needs it before the block can end, so this costs nothing).
+                for (int j = max(0, cc - G::kStages); j < cc; ++j)
+                    tc::mbar_wait(bar(G::KVFull + j % G::kStages), (j / G::kStages) & 1, never);
+                for (int j = max(0, qc - G::kQSlots); j < qc; ++j)
+                    tc::mbar_wait(bar(G::QFull + j % G::kQSlots), (j / G::kQSlots) & 1, never);
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ O stores (whole chunks)
@@ -410,7 +411,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                             tc::mma_commit(bar(G::WFree + wb));
                         }
                         if (!ok) break;
-                        tc::mma_commit(bar(G::UDone));
+                        if (!a.hold || blockIdx.x != 0) tc::mma_commit(bar(G::UDone));
                         tc::mma_commit(bar(G::KVEmpty + st));
                     }
                 }
@@ -494,7 +495,10 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 }
             }
         }
-        if (!ok) *abort = 1;
+        if (!ok) {
+            *abort = 1;
+            tc::tmem_wait_st();         // scores may be on their way to tensor memory, which is freed below
+        }
     } else if (warp < 12) {
         // ------------------------------------------------------------ K group
         // without queries the P group weighs every other piece of keys
@@ -722,6 +726,9 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         for (int i = blockIdx.x; i < a.nerr; i += gridDim.x) a.err[HB_IDX(i, a.nerr)] = i == (int)blockIdx.x ? *abort : 0;
 }
 
+// tests: a wait of block 0 runs out in every later launch (hyena_test_linattn_hold)
+std::atomic<int> g_hold{0};
+
 // [B][L][heads][width] bf16 with rows `ld` elements apart; boxes of 64 entries x 1 head x 128 tokens
 bool make_map(CUtensorMap *m, const void *base, int B, int L, int heads, int width, long long ld) {
     static PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
@@ -766,6 +773,8 @@ cudaError_t launch(const Maps &m, const LinArgs &a, int items, bool states_only,
 
 HYENA_BOUNDS_READER(linattn_tc)
 
+void linattn_hold(int enable) { g_hold.store(enable); }
+
 bool linattn_tc_dims(int dtype, int dk, int dv) { return dtype == HYENA_BF16 && dk <= 128 && dk % 8 == 0 && dv % 8 == 0; }
 
 // How a prompt is cut, by a model of the time in us (blocks take their items one after the other, so the longest one
@@ -805,7 +814,8 @@ LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens) 
     return best;
 }
 
-cudaError_t launch_linattn_tc(const LinArgs &a, bool states_only, cudaStream_t s) {
+cudaError_t launch_linattn_tc(LinArgs a, bool states_only, cudaStream_t s) {
+    a.hold = g_hold.load(std::memory_order_relaxed);
     const long long items = (long long)(states_only ? a.nseg - 1 : a.nseg) * a.B * a.Hk * a.vtiles;
     if (items > 0x7fffffffll - kLinMaxBlocks) return cudaErrorInvalidValue;
     Maps m;

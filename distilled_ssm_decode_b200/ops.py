@@ -64,6 +64,7 @@ SIGNATURES = {
     "hyena_linattn_prefill_workspace_bytes": (_sz, [_i] * 7),
     "hyena_linattn_prefill_error_offset": (_sz, [_i] * 7),
     "hyena_linattn_prefill_uses_tensor_cores": (_i, [_i] * 7 + [_ll] * 3 + [_vp] * 4),
+    "hyena_test_linattn_hold": (_i, [_i]),
     "hyena_linattn_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _fp, _vp, _fp,
                                    _vp, _sz, _vp]),
     "hyena_linattn_decode_step": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _ll, _ll, _ll, _fp, _f, _vp, _vp, _i, _fp,
@@ -658,6 +659,17 @@ def linattn_error(workspace, dtype, B, L, H, Hk, dk, dv) -> int:
     lo = int(lib().hyena_linattn_prefill_error_offset(_DT[dtype], B, L, H, Hk, dk, dv))
     hi = linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv)
     return int(workspace[lo:hi].view(torch.int32).abs().max().item())
+
+
+@contextlib.contextmanager
+def linattn_hold():
+    """Test hook: inside the block a bounded wait of every tensor-core linattn_prefill runs out (see
+    hyena.h)."""
+    _check("hyena_test_linattn_hold", lib().hyena_test_linattn_hold(1))
+    try:
+        yield
+    finally:
+        _check("hyena_test_linattn_hold", lib().hyena_test_linattn_hold(0))
 
 
 def linattn_decode_step(q, k, v, decay, state, scale: float = 1.0, prep: QKPrep = None, positions=None, pos0: int = 0,

@@ -484,6 +484,15 @@ int hyena_linattn_prefill(const void *q, const void *k, const void *v, int dtype
                           void *workspace, size_t ws_bytes, hyena_stream_t stream);
 
 /*
+ * Test hook (no counterpart in the pages): enable = 1 makes block 0 of every later
+ * tensor-core launch of hyena_linattn_prefill keep back the signal that its state products
+ * are done, so that a bounded wait runs out (after 2 s) without any GPU fault and the call's
+ * error words show it; 0 restores normal operation.  HYENA_ERR_ARG for other values.
+ * Process-wide; meant for tests only.
+ */
+int hyena_test_linattn_hold(int enable);
+
+/*
  * Norm of queries and keys for each head, and the position rotation, in one pass:
  *     x <- x * rsqrt(mean(x^2) + eps) * weight        (over one head's hd entries)
  *     (a, b) <- (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i]
