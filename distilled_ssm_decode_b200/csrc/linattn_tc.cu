@@ -57,10 +57,14 @@ constexpr int kBlk = kC * 128;          // bytes of a [128 tokens][64 entries] b
 constexpr uint32_t kColP = 0, kColO = 128, kColU = 256, kColW = 384;   // tensor-memory columns
 constexpr uint32_t kTmemCols = 512;
 constexpr int kTerms = 4;               // bf16 terms of a weighted key
-// Decays of kUp and more: the sums are kept divided by the row's factor, O / (scale g^(i+1)), so that Q S needs no
-// scaling and P's factor g^-(j+1) (at most 0.75^-128 < 2^54) depends on the column alone; the row's factor comes in
-// with the output's rounding.  Smaller decays would overflow there: they scale P by rows and columns and Q S in place.
-constexpr double kUp = 0.75;
+// Decays of kUp and more: the sums are kept as O g^(127-i) / scale, so that P's factor g^(127-j) depends on the column
+// alone and the state's copy takes the rest of Q S, g^128; the row's factor scale g^(i-127) comes in with the output's
+// rounding.  No factor inside the sums is above 1, so nothing passes fp32's range that the formula keeps inside it; at the
+// other end they are as small as g^127 > 2^-25, so that scores below 2^-101 count as 0.  Smaller decays would lose more
+// there (0.75: scores below 2^-73): they scale P by rows and columns and Q S in place, which costs another pass over
+// Q S.  us of the launches alone that way and this: 64 x 512 x 16 heads of 128 x 128 160 and 137, 8 x 4096 x 8 heads 131 and
+// 100, 65536 x 12 heads of 64 x 64 240 and 207.
+constexpr double kUp = 0.875;
 constexpr int kSub = 32;                // tokens of weighted keys in one of two buffers
 constexpr int kWBufs = 2, kWCols = kTerms * kSub / 2;
 static_assert(kColW + kWBufs * kWCols <= kTmemCols, "tensor memory");
@@ -103,6 +107,14 @@ struct Geo {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
+}
+
+// f lo, f hi in fp32 (one packed multiply), then as bf16
+__device__ __forceinline__ uint32_t pack2_scaled(float f, float lo, float hi) {
+    float a, b;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(a), "=f"(b) : "f"(lo), "f"(hi), "f"(f));
+    return pack2(a, b);
 }
 
 struct Item {
@@ -148,7 +160,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = tc::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float *pw = reinterpret_cast<float *>(sm + G::kSmPw);            // pw[x] = g^x, or g^-(x + 1) (the P group's)
+    float *pw = reinterpret_cast<float *>(sm + G::kSmPw);            // pw[x] = g^x, or g^(127 - x) (the P group's)
     PairWeights *rw = reinterpret_cast<PairWeights *>(pw + kC);      // rw[x]: g^(n - 1 - 2 x), g^(n - 2 - 2 x) (the K group's)
     volatile int *misc = reinterpret_cast<volatile int *>(sm + G::kSmMisc);   // abort (= error code), tensor memory, never
     volatile int *abort = misc, *never = misc + 2;
@@ -425,7 +437,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
         const int w = warp & 3, row = 32 * w + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
         int qc = 0, hk_cur = -1, met = 0;
-        float f_row = 0.f;          // scale g^(i+1) of this row
+        float f_row = 0.f;          // scale g^(i+1) of this row, or scale g^(i-127)
         bool up = false, ok = true;
         for (int id = blockIdx.x; id < items && ok; id += gridDim.x) {
             const Item it = item_of(a, id, NV);
@@ -434,8 +446,8 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                 if (!(ok = meet(G::PSync, met))) break;
                 const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
                 up = g >= kUp;
-                pw[row] = (float)decay_pow(up ? 1.0 / g : g, up ? row + 1 : row);
-                f_row = a.scale * (float)decay_pow(g, row + 1);
+                pw[row] = (float)decay_pow(g, up ? kC - 1 - row : row);
+                f_row = a.scale * (float)(up ? decay_pow(1.0 / g, kC - 1 - row) : decay_pow(g, row + 1));
                 if (!(ok = meet(G::PSync, met))) break;
                 hk_cur = it.hk;
             }
@@ -603,6 +615,7 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
             const Item it = item_of(a, id, NV);
             const double g = (double)a.decay[HB_IDX(it.hk, a.Hk)];
             const float g_all = (float)decay_pow(g, kC), g_last = (float)decay_pow(g, it.ntok - (it.nck - 1) * kC);
+            const float g_copy = g >= kUp ? g_all : 1.f;         // what the copy that multiplies the queries takes of Q S's factor
             const int col0 = it.c0 + sg * NH;
             const long long at = (((long long)it.b * a.Hk + it.hk) * a.dk + 32 * w) * a.dv + col0;       // this warp's rows
             const float *init = states_only || !a.init ? nullptr : a.init + (long long)it.seg * a.init_stride;
@@ -683,8 +696,8 @@ linattn_tc_kernel(const __grid_constant__ Maps m, const LinArgs a, const int ite
                         for (int i = 0; i < NH / 8; ++i) {
                             const int ch = sg * (NH / 8) + i;
                             *reinterpret_cast<uint4 *>(row + (ch / 8) * (NK * 128) + (((ch & 7) ^ (d & 7)) << 4)) =
-                                make_uint4(pack2(S[8 * i], S[8 * i + 1]), pack2(S[8 * i + 2], S[8 * i + 3]),
-                                           pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
+                                make_uint4(pack2_scaled(g_copy, S[8 * i], S[8 * i + 1]), pack2_scaled(g_copy, S[8 * i + 2], S[8 * i + 3]),
+                                           pack2_scaled(g_copy, S[8 * i + 4], S[8 * i + 5]), pack2_scaled(g_copy, S[8 * i + 6], S[8 * i + 7]));
                         }
                         tc::fence_proxy_async_smem();
                     }

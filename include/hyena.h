@@ -457,6 +457,9 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * chunks of 128 tokens, o from bf16 products with fp32 accumulation, the state in
  * fp32 (its products take the weighted keys as sums of four bf16 terms, which keep
  * them to 2^-25).  Every other call runs in fp32 on the CUDA cores.
+ * Range: scores q.k and the sums over tokens are fp32 numbers that scale multiplies last;
+ * no weight inside them is above 1, so they pass fp32's range only where the formula does.
+ * On the tensor-core route scores below 2^-101 may count as 0 for decays of 0.875 and more.
  * hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the error that
  * hyena_linattn_prefill would return); host-only.
  * The tensor-core route waits on its own copies and products with bounded
