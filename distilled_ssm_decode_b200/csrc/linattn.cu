@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_kernel(const LinArgs a, i
             }
         }
     }
+    // this route has no waits: its error words are 0
+    for (long long i = (long long)blockIdx.x * kThreads + tid; i < a.nerr; i += (long long)gridDim.x * kThreads) a.err[HB_IDX(i, a.nerr)] = 0;
     float *dst = states_only ? a.states + (long long)(seg + 1) * a.init_stride : seg == a.nseg - 1 ? a.state_out : nullptr;
     if (dst) {
 #pragma unroll

@@ -31,7 +31,7 @@ struct LinArgs {
     float *state_out;        // else: the state after the last segment
     int seg_tokens, nseg;    // segments of this launch (states_only leaves out the last one)
     int vtiles, nv;          // column tiles of a state, their width
-    int *err;                // tensor-core route: an error word for each block
+    int *err;                // an error word for each block of the tensor-core route (the other route clears them)
     int nerr;
     int hold;                // tests: block 0 never signals its state products, so that a wait runs out
 };

@@ -607,13 +607,29 @@ def linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv) -> int:
     return int(lib().hyena_linattn_prefill_workspace_bytes(_DT[dtype], B, L, H, Hk, dk, dv))
 
 
+class LinattnPrefill(tuple):
+    """(o, state) of linattn_prefill, which unpacks as the two tensors, with the call's workspace.  On the
+    tensor-core route the results hold only if error() is 0: its bounded waits report there."""
+
+    def __new__(cls, o, state, workspace, dims):
+        self = super().__new__(cls, (o, state))
+        self.workspace, self._dims = workspace, dims
+        return self
+
+    def error(self) -> int:
+        """0 when the call's every bounded wait succeeded (synchronises; before the workspace is used again)."""
+        return linattn_error(self.workspace, *self._dims)
+
+
 def linattn_prefill(q, k, v, decay, scale: float = 1.0, lens=None, state_in=None, o=None, state=None, workspace=None):
     """Linear attention with a decay for each head over a prompt: S_t = g S_{t-1} + k_t v_t^T,
     o_t = scale S_t^T q_t.
 
     q [B][L][H][dk], k [B][L][Hk][dk], v [B][L][Hk][dv] (slices of one projection work), decay float32
     [Hk], lens int32 [B] (tokens of each row; the rows of o behind them are left as they were, zero
-    if o is made here), state_in float32 [B][Hk][dk][dv].  Returns (o [B][L][H][dv], state)."""
+    if o is made here), state_in float32 [B][Hk][dk][dv].  Returns (o [B][L][H][dv], state), a
+    LinattnPrefill: its error() is 0 once the call has run, unless a bounded wait gave up and the results are
+    not valid."""
     dt, dev = _act_dtype(q), q.device
     dtype = q.dtype
     ldq, ldk, ldv = _rows(q, "q", 4, dtype, dev), _rows(k, "k", 4, dtype, dev), _rows(v, "v", 4, dtype, dev)
@@ -638,7 +654,7 @@ def linattn_prefill(q, k, v, decay, scale: float = 1.0, lens=None, state_in=None
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
     _run("hyena_linattn_prefill", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, B, L, H, Hk, dk, dv, ldq, ldk, ldv,
          decay_at, scale, lens_at, in_at, o_at, state_at, workspace.data_ptr(), workspace.numel())
-    return o, state
+    return LinattnPrefill(o, state, workspace, (dtype, B, L, H, Hk, dk, dv))
 
 
 def linattn_prefill_uses_tensor_cores(q, k, v, o=None) -> bool:
@@ -654,8 +670,9 @@ def linattn_prefill_uses_tensor_cores(q, k, v, o=None) -> bool:
 
 
 def linattn_error(workspace, dtype, B, L, H, Hk, dk, dv) -> int:
-    """The error words of linattn_prefill's tensor-core route (synchronises): 0 when every bounded wait
-    succeeded."""
+    """The error words of linattn_prefill (synchronises): 0 when every bounded wait succeeded."""
+    if B == 0 or L == 0:
+        return 0            # nothing ran
     lo = int(lib().hyena_linattn_prefill_error_offset(_DT[dtype], B, L, H, Hk, dk, dv))
     hi = linattn_prefill_workspace_bytes(dtype, B, L, H, Hk, dk, dv)
     return int(workspace[lo:hi].view(torch.int32).abs().max().item())

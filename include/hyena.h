@@ -457,16 +457,16 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * chunks of 128 tokens, o from bf16 products with fp32 accumulation, the state in
  * fp32 (its products take the weighted keys as sums of four bf16 terms, which keep
  * them to 2^-25).  Every other call runs in fp32 on the CUDA cores.
- * Range: scores q.k and the sums over tokens are fp32 numbers that scale multiplies last;
+ * Range: scores q.k, before scale multiplies them, and the sums over tokens are fp32 numbers;
  * no weight inside them is above 1, so they pass fp32's range only where the formula does.
  * On the tensor-core route scores below 2^-101 may count as 0 for decays of 0.875 and more.
  * hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the error that
  * hyena_linattn_prefill would return); host-only.
  * The tensor-core route waits on its own copies and products with bounded
  * waits: the int32s from byte hyena_linattn_prefill_error_offset() to the end of
- * the queried workspace are all 0 after a successful run of that route; another
- * value means that a wait gave up and the outputs are not valid.  (The other
- * route has no waits and leaves them as they were.)
+ * the queried workspace are all 0 after a successful run; another value means that
+ * a wait gave up and the outputs are not valid.  (The other route has no waits and
+ * clears them; empty problems leave the workspace alone.)
  * Values in q, k, v of a sequence's own tokens that are not finite may reach the
  * outputs of tokens up to a chunk earlier, too.
  * Empty problems (B == 0, or L == 0) are valid; L == 0 writes state_out.

@@ -32,3 +32,26 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_nothing_behind(B, L, H, d):
     o, st = ops.linattn_prefill(q, k, v, dec, scale=0.25, workspace=ws)
     assert ops.linattn_error(ws, *dims) == 0
     check(o, st, reference(q, k, v, dec, 0.25), L, d, BF16, True)
+
+
+def test_the_default_call_tells_of_a_wait_that_ran_out():
+    q, k, v, _ = (None if t is None else t.cuda() for t in inputs(1, 100, 2, 2, 64, 64, BF16, 3))
+    dec = decays(2).cuda()
+    with ops.linattn_hold():
+        r = ops.linattn_prefill(q, k, v, dec)
+        assert r.error() != 0
+    r = ops.linattn_prefill(q, k, v, dec)
+    o, st = r
+    assert r.error() == 0 and len(r) == 2 and o is r[0] and st is r[1]
+
+
+# fp32 takes the route without waits, cut (1, 3000) and in one piece; empty problems run nothing.
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("B,L", [(1, 3000), (2, 30), (2, 1), (2, 0), (0, 5)])
+def test_every_call_that_succeeds_says_so(dtype, B, L):
+    q, k, v, _ = (None if t is None else t.cuda() for t in inputs(B, L, 2, 2, 64, 64, dtype, 4))
+    dec = decays(2).cuda()
+    n = ops.linattn_prefill_workspace_bytes(dtype, B, L, 2, 2, 64, 64)
+    ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+    assert ops.linattn_prefill(q, k, v, dec, workspace=ws).error() == 0
+    assert ops.linattn_prefill(q, k, v, dec).error() == 0
