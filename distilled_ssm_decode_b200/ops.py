@@ -480,6 +480,9 @@ def modal_truncate(lam, R, k: int):
 # ------------------------------------------------------------------ linear attention
 # A token's step takes a few microseconds on the GPU, so the host side of these calls is kept short: pointers go
 # to ctypes as plain integers, the stream is read as a number, sizes of workspaces are looked up.
+_INT_MAX = 0x7fffffff     # the library's sizes and positions; ctypes would cut larger ones to their low bits
+
+
 def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
     """Row stride (elements between consecutive tokens) of q, k or v [B][L][heads][width] (dim 4) or
     [B][heads][width] (dim 3): heads and width contiguous, rows evenly spaced, as a slice of one
@@ -493,6 +496,8 @@ def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
     sh, st = t.shape, t.stride()
     if len(sh) != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
+    if max(sh) > _INT_MAX:
+        raise ValueError(f"{name}: sizes must fit 32 bits, got {list(sh)}")
     if dim == 3:
         rows, heads, width = sh
         s_row, s_head, s_entry = st
@@ -528,6 +533,12 @@ def _plain(t, name: str, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
+
+
+def _position(pos0):
+    if not -_INT_MAX - 1 <= pos0 <= _INT_MAX:
+        raise ValueError(f"pos0 must fit 32 bits, got {pos0}")
+    return pos0
 
 
 def _run(fn: str, device, *args):
@@ -598,7 +609,7 @@ def qk_norm_rotate(q, k, prep: QKPrep, positions=None, pos0: int = 0, q_out=None
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out and k_out must have the shapes of q and k")
     _run("hyena_qk_norm_rotate", dev, q.data_ptr(), k.data_ptr(), dt, B, L, H, Hk, hd, ldq, ldk, prep._check(hd, dev),
-         pos, pos0, q_out.data_ptr(), k_out.data_ptr(), ldqo, ldko)
+         pos, _position(pos0), q_out.data_ptr(), k_out.data_ptr(), ldqo, ldko)
     return q_out, k_out
 
 
@@ -714,5 +725,5 @@ def linattn_decode_step(q, k, v, decay, state, scale: float = 1.0, prep: QKPrep 
     else:
         o_at = _plain(o, "o", dtype, (B, H, dv), dev)
     _run("hyena_linattn_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, B, H, Hk, dk, dv, ldq, ldk, ldv,
-         decay_at, scale, None if prep is None else prep._check(dk, dev), pos, pos0, state_at, o_at)
+         decay_at, scale, None if prep is None else prep._check(dk, dev), pos, _position(pos0), state_at, o_at)
     return o

@@ -1,5 +1,6 @@
 """More argument checks of the linear-attention entry points (host only, as in test_linattn_cpu.py)."""
 import pytest
+import torch
 
 OK, ERR_ARG = 0, -1
 
@@ -14,3 +15,33 @@ def lib():
 def test_hold_hook_validates_its_argument(lib):
     assert lib.hyena_test_linattn_hold(2) == ERR_ARG and lib.hyena_test_linattn_hold(-1) == ERR_ARG
     assert lib.hyena_test_linattn_hold(0) == OK
+
+
+class _OnDevice(torch.Tensor):
+    """A stand-in that claims to be on the device: the checks before the library call run without a GPU."""
+    is_cuda = True
+
+
+@pytest.mark.parametrize("pos0", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1])
+def test_binding_refuses_positions_beyond_32_bits(monkeypatch, pos0):
+    """They reached the library cut to their low 32 bits: another position's angles."""
+    from distilled_ssm_decode_b200 import ops
+    monkeypatch.setattr(ops, "_run", lambda *a: pytest.fail("the library was called"))
+    x = torch.zeros((2, 3, 2, 8)).as_subclass(_OnDevice)
+    prep = ops.QKPrep()
+    with pytest.raises(ValueError, match="pos0"):
+        ops.qk_norm_rotate(x, x, prep, pos0=pos0)
+    with pytest.raises(ValueError, match="pos0"):
+        ops.linattn_decode_step(x[:, 0], x[:, 0], x[:, 0], torch.ones(2), torch.zeros((2, 2, 8, 8)), prep=prep, pos0=pos0)
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 2, 1, 1, 1), (1, (1 << 32) + 9, 1, 1), (1, 1, 1 << 31, 1)])
+def test_binding_refuses_sizes_beyond_32_bits(shape):
+    """As above: (2^32 + 2) rows became 2."""
+    from distilled_ssm_decode_b200 import ops
+    x = torch.zeros((1, 1, 1, 1)).expand(shape).as_subclass(_OnDevice)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops._rows(x, "q", 4, torch.float32, x.device)
+    if shape[1] == 1:
+        with pytest.raises(ValueError, match="32 bits"):
+            ops._rows(x[:, 0], "q", 3, torch.float32, x.device)
