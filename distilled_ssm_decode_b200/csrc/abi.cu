@@ -499,6 +499,8 @@ int hyena_linattn_prefill_uses_tensor_cores(int dtype, int B, int L, int H, int 
     int st = check_linattn(dtype, B, L, H, Hk, dk, dv);
     if (st == HYENA_OK) st = check_strides(H, Hk, dk, dv, ldq, ldk, ldv);
     if (st != HYENA_OK) return st;
+    const size_t ab = (dtype == HYENA_BF16) ? 2 : 4;
+    if (!aligned(q, ab) || !aligned(k, ab) || !aligned(v, ab) || !aligned(o, ab)) return HYENA_ERR_ALIGN;
     return linattn_uses_tc(dtype, L, H, Hk, dk, dv, ldq, ldk, ldv, q, k, v, o) ? 1 : 0;
 }
 

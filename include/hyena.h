@@ -461,7 +461,8 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * no weight inside them is above 1, so they pass fp32's range only where the formula does.
  * On the tensor-core route scores below 2^-101 may count as 0 for decays of 0.875 and more.
  * hyena_linattn_prefill_uses_tensor_cores() tells which (1 or 0, or the error that
- * hyena_linattn_prefill would return); host-only.
+ * hyena_linattn_prefill would return for these arguments; NULL stands for an aligned
+ * pointer); host-only.
  * The tensor-core route waits on its own copies and products with bounded
  * waits: the int32s from byte hyena_linattn_prefill_error_offset() to the end of
  * the queried workspace are all 0 after a successful run; another value means that

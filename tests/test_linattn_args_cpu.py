@@ -1,8 +1,11 @@
 """More argument checks of the linear-attention entry points (host only, as in test_linattn_cpu.py)."""
+import ctypes
+
 import pytest
 import torch
 
-OK, ERR_ARG = 0, -1
+OK, ERR_ARG, ERR_ALIGN, ERR_CUDA = 0, -1, -3, -6
+FAKE = 1 << 40          # aligned, never dereferenced
 
 
 @pytest.fixture(scope="module")
@@ -45,3 +48,23 @@ def test_binding_refuses_sizes_beyond_32_bits(shape):
     if shape[1] == 1:
         with pytest.raises(ValueError, match="32 bits"):
             ops._rows(x[:, 0], "q", 3, torch.float32, x.device)
+
+
+def test_route_query_gives_the_calls_alignment_errors(lib):
+    """The query's documented answer: 1, 0, or the error that the call would return for these arguments."""
+    p = ctypes.c_void_p
+
+    def both(dtype=1, **at):
+        q, k, v, o = (at.get(n, FAKE) for n in "qkvo")
+        r = lib.hyena_linattn_prefill_uses_tensor_cores(dtype, 2, 16, 4, 2, 64, 64, 256, 128, 128, p(q), p(k), p(v), p(o))
+        c = lib.hyena_linattn_prefill(p(q), p(k), p(v), dtype, 2, 16, 4, 2, 64, 64, 256, 128, 128, p(FAKE), 1.0, None, None,
+                                      p(o), p(FAKE), p(FAKE), 1 << 40, None)
+        return r, c
+    for n in "qkvo":
+        assert both(**{n: FAKE + 1}) == (ERR_ALIGN, ERR_ALIGN), n
+        assert both(dtype=0, **{n: FAKE + 2}) == (ERR_ALIGN, ERR_ALIGN), n
+    assert lib.hyena_test_fail_next_launches(2) == OK
+    try:
+        assert both() == (1, ERR_CUDA) and both(q=FAKE + 2) == (0, ERR_CUDA)
+    finally:
+        lib.hyena_test_fail_next_launches(0)
