@@ -468,8 +468,11 @@ int hyena_modal_truncate(const float *lambda, const float *R, int H, int d, int 
  * the queried workspace are all 0 after a successful run; another value means that
  * a wait gave up and the outputs are not valid.  (The other route has no waits and
  * clears them; empty problems leave the workspace alone.)
- * Values in q, k, v of a sequence's own tokens that are not finite may reach the
- * outputs of tokens up to a chunk earlier, too.
+ * A value of a sequence's own tokens that is not finite stays where the formula takes it:
+ * one in q in its token's output, one in k in its row of the state, one in v in its column;
+ * from k and v it may reach the outputs of tokens up to a chunk earlier, too.  What it
+ * reaches is not finite, but the tensor-core route gives NaN where the formula and the
+ * CUDA cores may give an infinity (the remainder terms of a weighted key are 0 or inf - inf).
  * Empty problems (B == 0, or L == 0) are valid; L == 0 writes state_out.
  */
 #define HYENA_MAX_HEAD_DIM 256
