@@ -496,7 +496,7 @@ def _rows(t: torch.Tensor, name: str, dim: int, dtype, device):
     sh, st = t.shape, t.stride()
     if len(sh) != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    if max(sh) > _INT_MAX:
+    if t.numel() > _INT_MAX and max(sh) > _INT_MAX:
         raise ValueError(f"{name}: sizes must fit 32 bits, got {list(sh)}")
     if dim == 3:
         rows, heads, width = sh
