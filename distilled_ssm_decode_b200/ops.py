@@ -627,6 +627,9 @@ class LinattnPrefill(tuple):
         self.workspace, self._dims = workspace, dims
         return self
 
+    def __reduce__(self):
+        return tuple, (tuple(self),)          # copies are of the two tensors alone
+
     def error(self) -> int:
         """0 when the call's every bounded wait succeeded (synchronises; before the workspace is used again)."""
         return linattn_error(self.workspace, *self._dims)

@@ -68,3 +68,14 @@ def test_route_query_gives_the_calls_alignment_errors(lib):
         assert both() == (1, ERR_CUDA) and both(q=FAKE + 2) == (0, ERR_CUDA)
     finally:
         lib.hyena_test_fail_next_launches(0)
+
+
+def test_a_prefill_result_is_a_pair_also_when_copied():
+    import copy
+    import pickle
+    from distilled_ssm_decode_b200 import ops
+    o, s = torch.ones(2), torch.zeros(3)
+    r = ops.LinattnPrefill(o, s, torch.zeros(1), (torch.float32, 0, 0, 1, 1, 1, 1))
+    assert r == (o, s) and r.error() == 0
+    for c in (copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert len(c) == 2 and torch.equal(c[0], o) and torch.equal(c[1], s)
