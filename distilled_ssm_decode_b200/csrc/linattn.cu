@@ -280,6 +280,7 @@ bool linattn_uses_tc(int dtype, int L, int H, int Hk, int dk, int dv, long long 
     // A prompt of one block of tokens (kT) costs the CUDA cores less than the tensor cores' pipeline takes to fill:
     // 64 x 16 states of 128 x 128, carried, 8 tokens 52 us against 100, 16 tokens 85 against 101; 31 x 12 of 64 x 128 with 3
     // query heads each, 8 tokens 23 against 31 (16: 40); 200 x 8 of 128 x 128 with 4, 8 tokens 184 against 117.
+    // (The rule does not ask whether a state is carried: without one the tensor cores took 44 for the first of these.)
     if (L <= kT && (long long)L * (H / Hk) <= 3 * kT) return false;
     return linattn_tc_dims(dtype, dk, dv) && ldq % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0 && ok(q) && ok(k) && ok(v) && ok(o);
 }

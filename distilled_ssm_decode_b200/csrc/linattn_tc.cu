@@ -12,7 +12,8 @@
 //   Q S     128 x dv x dk    Q (shared) x S as bf16 (shared)    -> columns kColO, then scaled in place
 //   P V     128 x dv x n     P as bf16 (tensor memory, over the scores) x V (shared), onto kColO
 //   state   dk x dv x n      weighted keys (tensor memory) x V (shared), from zero -> kColU
-// Roundings to bf16: the scores' P and the state's copy that multiplies q (operands only; both reach o, itself bf16).
+// Roundings to bf16: the scores' P and the state's copy that multiplies q (operands only; both reach o, itself bf16: its error
+// in the 2-norm is 2.3e-3 where one rounding of the exact value leaves 1.7e-3; a second term for each would double two products).
 // The state itself stays fp32, in registers; its weighted keys enter as the sum of four bf16 terms, which keeps them to
 // 2^-25: one term would leave 2^-9, two 2^-17 of each token in a state that every later token reads.  A chunk's
 // contribution is summed from zero and joined by one fp32 multiply-add: summing onto the state in tensor memory
@@ -30,8 +31,8 @@
 // drains its copies and products, frees tensor memory and returns.
 //
 // Measured (us of the launches alone, bf16): 64 sequences x 512 tokens x 16 heads of 128 x 128 138 (67% of measured HBM),
-// 8 x 4096 x 8 heads 93 (45%), 65536 x 12 heads of 64 x 64 195 (32%: a second pass over K and V for the states).  What holds
-// it there is the length of a chunk's chains, not a unit: tensor cores 42% busy, issue slots 45%; a chunk takes 5.0 us where
+// 8 x 4096 x 8 heads 95 (44%), 65536 x 12 heads of 64 x 64 199 (31%: a second pass over K and V for the states).  What holds
+// it there is the length of a chunk's chains, not a unit: tensor cores 39% busy, issue slots 45%; a chunk takes 5.0 us where
 // its bytes take 3.0.  What was tried and not kept: the outputs by the S groups (their row of the state spills: 141 ->
 // 160), sleeping waits (no change), scores and state rows loaded two pieces ahead (185: spills), the next head's
 // powers computed ahead (142).
@@ -774,6 +775,7 @@ cudaError_t launch(const Maps &m, const LinArgs &a, int items, bool states_only,
         if (e != cudaSuccess) return e;
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, linattn_tc_kernel<NK, NV>)) != cudaSuccess) return e;
+        // 640 threads leave at most 96 registers each, the shares need at least 94, and counts come in eights: only 96 will do
         if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
     }
@@ -795,8 +797,12 @@ bool linattn_tc_dims(int dtype, int dk, int dv) { return dtype == HYENA_BF16 && 
 // `state`, the entry of an item (its state, the filling of the pipeline) `entry`; cutting adds the state pass, the
 // combination of the states and two launches.  Narrow tiles repeat the scores and the weighing of the keys, but give twice
 // the items: where sequences x heads leave SMs idle they cost less than a second pass over the tokens.
-// The figures were measured on whole grids when the rule was made; since then the passes have become faster by a tenth
-// (128 x 128 5.0 us a chunk, 128 x 64 2.9, 64 x 64 3.0 and 1.9 without queries), in proportion enough to leave the choices.
+// The figures were measured on whole grids when the rule was made.  Now a chunk takes 5.0 us (128 x 128), 3.0 (128 x 64, and
+// 64 x 64) or 1.9 (64 x 64 without queries), and an item's entry hides behind the item before, so the model reads 1.1 to 1.7
+// times too high (210, 134 and 285 us for the three shapes at the top of this file) and serves to compare cuts only.  The choices were compared
+// with both widths and 1 to 64 segments on eleven shapes: the fastest, or within 2 us of it, on ten (few sequences, one
+// long prompt, shared heads, a padded batch of 32 rows); 13 padded rows of 1537 tokens x 4 x 3 heads of 96 x 80 take 96 us
+// in the rule's five segments and 78 in four.
 // Padded rows (lens) are taken to be half full.
 LinPlan linattn_tc_plan(int B, int L, int H, int Hk, int dk, int dv, bool lens) {
     struct Cost { double base, query, state, entry; };
